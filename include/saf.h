@@ -269,6 +269,136 @@ SAF_API saf_status saf_attn_calibration(const void *q, const void *k, const floa
                                         void *workspace, size_t workspace_bytes,
                                         void *stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: a paged key/value cache for the layer.  Prompts are prefilled with
+ * saf_mixed_attn_fwd and appended; then each step appends its new tokens and
+ * attends over the cache.  Both head kinds keep their meaning: a replaced head
+ * has no query/key path, so its q is neither rotated nor read, and a K/V head
+ * whose query heads are all replaced keeps no keys (its K slots are neither
+ * written nor read).
+ *
+ * Conventions shared by these entry points
+ *   Cache      K and V pages, bf16.  Element (page, kv head, slot, c) of K is
+ *              k[page * k_stride_page + head * k_stride_head + slot * k_stride_slot + c]
+ *              (strides in elements), V likewise: a page may be stored heads
+ *              first or slots first, or be part of a larger tensor.  The bases
+ *              are 16-byte aligned and the strides multiples of 8 elements, at
+ *              least 64.  page_size is 16, 32, 64, 128 or 256.
+ *   Tables     page_table: [B, max_pages] int32 device; position p of sequence
+ *              b lives in page page_table[b, p / page_size], slot
+ *              p % page_size.  An entry outside [0, num_pages) is no page: its
+ *              tokens are not stored, and its keys take no part in a softmax.
+ *              Entries past a sequence's length are not used.
+ *   Lengths    seq_lens: [B] int32 device, tokens of each sequence in the cache
+ *              INCLUDING the call's new ones.  q_lens: [B] int32 device, new
+ *              tokens of each sequence (0 .. T_q; other values are clamped), or
+ *              NULL for T_q each.  New token t < q_lens[b] has position
+ *              seq_lens[b] - q_lens[b] + t; rows t >= q_lens[b] of the outputs
+ *              are left as they were.  max_len (host) bounds the lengths: it
+ *              sizes the launch, is at most max_pages * page_size, and no
+ *              position at or past it is read or written.
+ *   Captures   No call reads device data on the host, so calls can be captured
+ *              into a CUDA graph and replayed with new lengths and tables.
+ * ------------------------------------------------------------------------ */
+typedef struct saf_paged_kv {
+    void *k, *v;             /* device, bf16 */
+    int64_t k_stride_page, k_stride_head, k_stride_slot;
+    int64_t v_stride_page, v_stride_head, v_stride_slot;
+    int32_t num_pages, page_size, H_kv, d_h;
+} saf_paged_kv;
+
+/*
+ * Rotation table for saf_kv_append: table[p, i] = cos(p w_i), table[p, rot_dim/2 + i]
+ * = sin(p w_i) for p < max_pos, i < rot_dim/2, w_i = base^(-2 i / rot_dim); the
+ * angles are formed in 64 bits.  table: [max_pos, rot_dim] fp32 device out.
+ * rot_dim is 16, 32, 48 or 64; base > 0.  A caller with another frequency
+ * scheme fills the table itself.
+ */
+SAF_API saf_status saf_rope_table(float *table, int max_pos, int rot_dim, double base, void *stream);
+
+/*
+ * Appends new tokens to the cache, rotating queries and keys by position.
+ *   q        [B,H,T,d_h], k, v [B,H_kv,T,d_h] bf16 in, each with strides in
+ *            elements for (batch, head, token), multiples of 8 (so that slices
+ *            of one projection's output serve); the last axis is contiguous.
+ *   q_out    [B,H,T,d_h] bf16 out, contiguous: the rotated queries (rows of
+ *            replaced heads are left as they were).  q and q_out may both be
+ *            NULL.
+ *   k_out    [B,H_kv,T,d_h] bf16 out, contiguous, or NULL: the rotated keys
+ *            beside the cache, for a prefill by saf_mixed_attn_fwd.
+ *   rope     [rope_len, rot_dim] fp32 (see saf_rope_table), or NULL: nothing is
+ *            rotated.  The first rot_dim of the 64 columns are rotated in pairs
+ *            (i, i + rot_dim/2), or (2i, 2i+1) with interleaved != 0, by row
+ *            pos_offset + position; y0 = x0 cos - x1 sin, y1 = x1 cos + x0 sin in
+ *            fp32, rounded once.  rope_len >= pos_offset + max_len.
+ *   replaced_mask  host [H], or NULL: every head ordinary.
+ * Tokens whose position is outside [0, max_len) are skipped.  Two tokens with
+ * the same page and slot: one of the two is kept.  One launch.
+ */
+SAF_API saf_status saf_kv_append(const saf_paged_kv *kv,
+                                 const void *q, const int64_t *q_strides,
+                                 const void *k, const int64_t *k_strides,
+                                 const void *v, const int64_t *v_strides,
+                                 void *q_out, void *k_out,
+                                 const float *rope, int rope_len, int rot_dim, int interleaved, int pos_offset,
+                                 const uint8_t *replaced_mask,
+                                 const int32_t *page_table, int max_pages,
+                                 const int32_t *seq_lens, const int32_t *q_lens,
+                                 int B, int H, int T, int max_len, void *stream);
+
+/*
+ * Attention of T_q new tokens of each sequence over the cache (which holds
+ * them already).  The row of head h and new token t with position i sees the
+ * keys j <= i, j < seq_lens[b]:
+ *   ordinary head   s(j) = q . k_j / sqrt(d_h)
+ *   replaced head   s(j) = a[h, j] + r[h, i - j]   (Eq. (3): the softmax below is
+ *                   the pattern's row i, and lse is log Z(i))
+ *   lse = log sum_j exp(s(j)),   o = sum_j exp(s(j) - lse) v_j.
+ * A row that sees no key, or whose every score is -inf, gives o = 0, lse = -inf.
+ * Query head h reads K/V head h / (H / H_kv).
+ *   q        [B,H,T_q,d_h] bf16 (rows of replaced heads are not read)
+ *   o        [B,H,T_q,d_h] bf16 out;  lse [B,H,T_q] fp32 out.
+ *   a, r     [H, pattern_len] fp32, read for replaced heads only; with any
+ *            replaced head pattern_len >= max_len.
+ *   workspace  at least saf_paged_workspace_size(B,H,H_kv,T_q,0) bytes, 256-byte
+ *            aligned, of the serving calls alone: zeroed once before first use
+ *            (every call leaves its counters zero again), not shared with the
+ *            layer's entry points, and not used by two calls at once.
+ * Slots at or past a sequence's length may hold anything, NaN included.  A V
+ * value that one row of a call sees must be finite if another row of the same
+ * sequence must not see it (T_q > 1): a hidden key has weight zero, and zero
+ * times an infinity is not zero.
+ */
+SAF_API size_t saf_paged_workspace_size(int B, int H, int H_kv, int T_q, int prefix_len);
+SAF_API saf_status saf_paged_attn(const saf_paged_kv *kv, const void *q, void *o, float *lse,
+                                  const float *a, const float *r, int pattern_len,
+                                  const uint8_t *replaced_mask,
+                                  const int32_t *page_table, int max_pages,
+                                  const int32_t *seq_lens, const int32_t *q_lens,
+                                  int B, int H, int T_q, int max_len,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same for a batch whose sequences all begin with one shared prefix of
+ * prefix_len tokens (host value), stored once: position p < prefix_len of every
+ * sequence lives in page prefix_table[p / page_size], slot p % page_size
+ * (prefix_table: device, ceil(prefix_len / page_size) entries), and seq_lens,
+ * q_lens, page_table and max_len describe what follows it (local position p is
+ * position prefix_len + p).  The prefix is read once for the whole batch.
+ * pattern_len >= prefix_len + max_len with any replaced head.  prefix_len = 0 is
+ * saf_paged_attn.  saf_kv_append takes the local tables and lengths with
+ * pos_offset = prefix_len.  Workspace: saf_paged_workspace_size with this
+ * prefix_len (or a larger one).
+ */
+SAF_API saf_status saf_paged_attn_prefix(const saf_paged_kv *kv, const void *q, void *o, float *lse,
+                                         const float *a, const float *r, int pattern_len,
+                                         const uint8_t *replaced_mask,
+                                         const int32_t *prefix_table, int prefix_len,
+                                         const int32_t *page_table, int max_pages,
+                                         const int32_t *seq_lens, const int32_t *q_lens,
+                                         int B, int H, int T_q, int max_len,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * Reads (synchronously: waits for `stream`) and clears the device error word
  * that the kernels keep in the first 256 bytes of `workspace` (zero before

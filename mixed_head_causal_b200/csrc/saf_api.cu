@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "saf_common.cuh"
+#include "saf_paged.cuh"
 
 using namespace saf;
 
@@ -59,6 +60,47 @@ saf_status check_groups(int H, int H_kv) {
 bool force_mma_path() {
     const char* e = getenv("SAF_FORCE_MMA");
     return e && e[0] == '1';
+}
+
+// ------------------------------------------------------------- serving calls
+saf_status check_paged_kv(const saf_paged_kv* kv, int H) {
+    if (!kv) return SAF_ERR_INVALID_ARG;
+    if (kv->d_h != kHeadDim) return SAF_ERR_UNSUPPORTED;
+    if (kv->page_size < 16 || kv->page_size > 256 || (kv->page_size & (kv->page_size - 1))) return SAF_ERR_UNSUPPORTED;
+    if (kv->num_pages < 0) return SAF_ERR_INVALID_ARG;
+    const saf_status st = check_groups(H, kv->H_kv);
+    if (st != SAF_OK) return st;
+    if (!kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return SAF_ERR_INVALID_ARG;
+    const int64_t strides[6] = {kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot,
+                                kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot};
+    for (int64_t x : strides)  // below 2^38 elements, as a tensor map's strides are below 2^40 bytes
+        if (x < kHeadDim || (x & 7) || x >= (1ll << 38)) return SAF_ERR_INVALID_ARG;
+    return SAF_OK;
+}
+
+// Page tables and lengths of B sequences (B > 0) of T new tokens each.
+saf_status check_tables(const saf_paged_kv& kv, const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                        int max_len) {
+    if (max_pages < 0 || max_len < 0 || max_len > (int64_t)max_pages * kv.page_size) return SAF_ERR_INVALID_ARG;
+    if (!seq_lens || (max_len > 0 && !page_table)) return SAF_ERR_INVALID_ARG;
+    return SAF_OK;
+}
+
+HeadBits head_bits(const uint8_t* mask, int H) {
+    HeadBits hb{};
+    if (mask)
+        for (int h = 0; h < H; ++h)
+            if (mask[h]) hb.w[h >> 5] |= 1u << (h & 31);
+    return hb;
+}
+
+bool copy_strides(const int64_t* src, int64_t (&dst)[3]) {
+    if (!src) return false;
+    for (int i = 0; i < 3; ++i) {
+        if (src[i] < 0 || (src[i] & 7)) return false;
+        dst[i] = src[i];
+    }
+    return true;
 }
 
 }  // namespace
@@ -310,6 +352,133 @@ saf_status saf_replaced_pattern_grad(const void* v, const void* dout, const floa
     return cuda_status(launch_pattern_grad(static_cast<const __nv_bfloat16*>(v),
                                            static_cast<const __nv_bfloat16*>(dout), a, r, lz, hl, B, H, T, da, dr,
                                            s));
+}
+
+saf_status saf_rope_table(float* table, int max_pos, int rot_dim, double base, void* stream) {
+    if (max_pos < 0 || !(base > 0.0)) return SAF_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return SAF_ERR_UNSUPPORTED;
+    if (max_pos == 0) return SAF_OK;
+    if (!table || !aligned16(table)) return SAF_ERR_INVALID_ARG;
+    return cuda_status(launch_rope_table(table, max_pos, rot_dim, base, (cudaStream_t)stream));
+}
+
+saf_status saf_kv_append(const saf_paged_kv* kv, const void* q, const int64_t* q_strides, const void* k,
+                         const int64_t* k_strides, const void* v, const int64_t* v_strides, void* q_out, void* k_out,
+                         const float* rope, int rope_len, int rot_dim, int interleaved, int pos_offset,
+                         const uint8_t* replaced_mask, const int32_t* page_table, int max_pages,
+                         const int32_t* seq_lens, const int32_t* q_lens, int B, int H, int T, int max_len,
+                         void* stream) {
+    if (!kv) return SAF_ERR_INVALID_ARG;
+    saf_status st = check_shape(B, H, T, kv->d_h);
+    if (st != SAF_OK) return st;
+    st = check_paged_kv(kv, H);
+    if (st != SAF_OK) return st;
+    if ((int64_t)B * H * T == 0) return SAF_OK;
+    st = check_tables(*kv, page_table, max_pages, seq_lens, max_len);
+    if (st != SAF_OK) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || (q == nullptr) != (q_out == nullptr)) return SAF_ERR_INVALID_ARG;
+    if ((q && (!aligned16(q) || !aligned16(q_out))) || (k_out && !aligned16(k_out))) return SAF_ERR_INVALID_ARG;
+    if (pos_offset < 0) return SAF_ERR_INVALID_ARG;
+    if (rope) {
+        if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return SAF_ERR_UNSUPPORTED;
+        if (!aligned16(rope) || rope_len < (int64_t)pos_offset + max_len) return SAF_ERR_INVALID_ARG;
+    }
+    // eight threads per row, 256 per block, fewer than 2^31 blocks
+    if ((double)B * T * (H + 2 * kv->H_kv) >= 32.0 * INT_MAX) return SAF_ERR_INVALID_ARG;
+    AppendParams p{};
+    if (!copy_strides(k_strides, p.ks) || !copy_strides(v_strides, p.vs) || (q && !copy_strides(q_strides, p.qs)))
+        return SAF_ERR_INVALID_ARG;
+    p.kv = *kv;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
+    p.rope = rope;
+    p.rot_dim = rope ? rot_dim : 0;
+    p.interleaved = interleaved ? 1 : 0;
+    p.pos_offset = pos_offset;
+    p.replaced = head_bits(replaced_mask, H);
+    const int group = H / kv->H_kv;
+    for (int g = 0; g < kv->H_kv; ++g) {
+        bool keyed = false;
+        for (int u = 0; u < group; ++u) keyed |= !p.replaced.get(g * group + u);
+        if (!keyed) p.keyless.w[g >> 5] |= 1u << (g & 31);
+    }
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.q_lens = q_lens;
+    p.max_pages = max_pages;
+    p.B = B;
+    p.H = H;
+    p.T = T;
+    p.max_len = max_len;
+    return cuda_status(launch_kv_append(p, (cudaStream_t)stream));
+}
+
+size_t saf_paged_workspace_size(int B, int H, int H_kv, int T_q, int prefix_len) {
+    if (check_shape(B, H, T_q, kHeadDim) != SAF_OK || check_groups(H, H_kv) != SAF_OK || prefix_len < 0)
+        return (size_t)-1;
+    if ((int64_t)B * H * T_q == 0) return 0;
+    return paged_workspace_bytes(B, H, H_kv, T_q, prefix_len);
+}
+
+saf_status saf_paged_attn_prefix(const saf_paged_kv* kv, const void* q, void* o, float* lse, const float* a,
+                                 const float* r, int pattern_len, const uint8_t* replaced_mask,
+                                 const int32_t* prefix_table, int prefix_len, const int32_t* page_table, int max_pages,
+                                 const int32_t* seq_lens, const int32_t* q_lens, int B, int H, int T_q, int max_len,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    if (!kv) return SAF_ERR_INVALID_ARG;
+    saf_status st = check_shape(B, H, T_q, kv->d_h);
+    if (st != SAF_OK) return st;
+    st = check_paged_kv(kv, H);
+    if (st != SAF_OK) return st;
+    if (prefix_len < 0) return SAF_ERR_INVALID_ARG;
+    if ((int64_t)B * H * T_q == 0) return SAF_OK;
+    st = check_tables(*kv, page_table, max_pages, seq_lens, max_len);
+    if (st != SAF_OK) return st;
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return SAF_ERR_INVALID_ARG;
+    if (prefix_len > 0 && !prefix_table) return SAF_ERR_INVALID_ARG;
+    // positions, and rows of one K/V head over the batch, in 32 bits
+    if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || (int64_t)B * H * T_q > INT_MAX / 128) return SAF_ERR_INVALID_ARG;
+    PagedParams p{};
+    p.replaced = head_bits(replaced_mask, H);
+    bool any = false;
+    for (uint32_t w : p.replaced.w) any |= w != 0;
+    if (any) {
+        if (!a || !r || !aligned16(a) || !aligned16(r)) return SAF_ERR_INVALID_ARG;
+        if (pattern_len < (int64_t)prefix_len + max_len) return SAF_ERR_INVALID_ARG;
+    }
+    if (!workspace || workspace_bytes < paged_workspace_bytes(B, H, kv->H_kv, T_q, prefix_len)) return SAF_ERR_WORKSPACE;
+    if (!aligned256(workspace)) return SAF_ERR_INVALID_ARG;
+    p.kv = *kv;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.a = a;
+    p.r = r;
+    p.pattern_len = pattern_len;
+    p.prefix_table = prefix_table;
+    p.prefix_len = prefix_len;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.q_lens = q_lens;
+    p.max_pages = max_pages;
+    p.B = B;
+    p.H = H;
+    p.T = T_q;
+    p.max_len = max_len;
+    p.ws = static_cast<char*>(workspace);
+    const cudaError_t e = launch_paged_attn(p, (cudaStream_t)stream);
+    return e == cudaErrorNotSupported ? SAF_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+saf_status saf_paged_attn(const saf_paged_kv* kv, const void* q, void* o, float* lse, const float* a, const float* r,
+                          int pattern_len, const uint8_t* replaced_mask, const int32_t* page_table, int max_pages,
+                          const int32_t* seq_lens, const int32_t* q_lens, int B, int H, int T_q, int max_len,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    return saf_paged_attn_prefix(kv, q, o, lse, a, r, pattern_len, replaced_mask, nullptr, 0, page_table, max_pages,
+                                 seq_lens, q_lens, B, H, T_q, max_len, workspace, workspace_bytes, stream);
 }
 
 saf_status saf_selftest_wait_timeout(void* workspace, size_t workspace_bytes, long long limit_cycles,

@@ -23,7 +23,8 @@ struct Profile {
 } g_prof;
 
 const char* kNames[] = {"?", "pattern", "fwd_mma", "dot", "dkdv_mma", "dq_mma",
-                        "fwd_tc", "bwd_tc", "(retired)", "dq_convert", "bwd_pre", "group_sum", "pattern_grad", "calibration", "fit"};
+                        "fwd_tc", "bwd_tc", "(retired)", "dq_convert", "bwd_pre", "group_sum", "pattern_grad", "calibration", "fit",
+                        "rope_table", "kv_append", "paged_attn"};
 
 void release_locked() {
     for (auto& r : g_prof.recs) {

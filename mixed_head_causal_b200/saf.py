@@ -44,6 +44,13 @@ SIGNATURES = {
     "saf_attn_calibration": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp], _i),
     "saf_mixed_attn_bwd_noalloc": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                     _vp, _vp, _vp, _i, _vp], _i),
+    "saf_rope_table": ([_vp, _i, _i, ctypes.c_double, _vp], _i),
+    "saf_kv_append": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp,
+                       _i, _i, _i, _i, _vp], _i),
+    "saf_paged_workspace_size": ([_i, _i, _i, _i, _i], _sz),
+    "saf_paged_attn": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp], _i),
+    "saf_paged_attn_prefix": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i,
+                               _vp, _sz, _vp], _i),
     "saf_launch_count": ([], ctypes.c_uint64),
     "saf_profile_enable": ([_i], _i),
     "saf_profile_read": ([ctypes.POINTER(_i), ctypes.POINTER(ctypes.c_float), _i], _i),
@@ -315,6 +322,243 @@ def mixed_attn_bwd_noalloc(q, k, v, o, dout, lse, alpha, rho, mask, logz=None, g
                                              B, H, T, d, _ptr(dq), _ptr(dk), _ptr(dv), gd, _stream_ptr(stream)),
            "saf_mixed_attn_bwd_noalloc")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ serving
+class _PagedKVStruct(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp)] + [(f"{t}_stride_{a}", ctypes.c_int64) for t in "kv"
+                                           for a in ("page", "head", "slot")] + [
+        (n, ctypes.c_int32) for n in ("num_pages", "page_size", "H_kv", "d_h")]
+
+
+class PagedKV:
+    """A paged key/value cache: k_cache, v_cache bf16 CUDA tensors of logical
+    shape [num_pages, H_kv, page_size, 64] with a contiguous last axis and any
+    other strides (pages may be stored slots first, or be slices of a larger
+    tensor).  Made once and passed to the serving calls."""
+
+    def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor):
+        for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 4 or t.shape[3] != HEAD_DIM or t.stride(3) != 1:
+                raise ValueError(f"{n}: expected a CUDA bf16 [num_pages, H_kv, page_size, {HEAD_DIM}] tensor with a "
+                                 f"contiguous last axis, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+        if k_cache.shape != v_cache.shape or k_cache.device != v_cache.device:
+            raise ValueError("k_cache and v_cache differ in shape or device")
+        self.k_cache, self.v_cache = k_cache, v_cache
+        self.device = k_cache.device
+        self.num_pages, self.h_kv, self.page_size, _ = k_cache.shape
+        # the stride of an axis of one entry is never used: any valid one will do
+        strides = [HEAD_DIM if t.shape[i] <= 1 else t.stride(i) for t in (k_cache, v_cache) for i in range(3)]
+        self._struct = _PagedKVStruct(k_cache.data_ptr(), v_cache.data_ptr(), *strides, self.num_pages, self.page_size,
+                                      self.h_kv, HEAD_DIM)
+        self._addr = ctypes.addressof(self._struct)
+
+
+def head_mask(mask) -> bytes:
+    """A replaced-head mask as the bytes the library reads; made once, it
+    spares the serving calls the conversion."""
+    if isinstance(mask, bytes):
+        return mask
+    buf, n = _mask_buffer(mask)
+    return bytes(buf)[:n]
+
+
+def _check_serving_tensors(device, tensors) -> None:
+    """(name, tensor, dtype, shape) of each: contiguous, on `device`."""
+    for name, t, dtype, shape in tensors:
+        if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on {device}, "
+                             f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _check_tables(kv, page_table, seq_lens, q_lens, B, max_len) -> int:
+    tables = [("page_table", page_table, torch.int32, (B, page_table.shape[-1])), ("seq_lens", seq_lens, torch.int32, (B,))]
+    if q_lens is not None:
+        tables.append(("q_lens", q_lens, torch.int32, (B,)))
+    _check_serving_tensors(kv.device, tables)
+    return page_table.shape[1] * kv.page_size if max_len is None else max_len
+
+
+class _Serving:
+    """The device and stream of a serving call: the cache's device is made
+    current, and what the call allocates belongs to the stream it runs on."""
+
+    def __init__(self, device, stream):
+        self._guards = []
+        if device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self._guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+@_annotated
+def rope_table(max_pos: int, rot_dim: int = HEAD_DIM, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:
+    """Rotation table [max_pos, rot_dim] fp32 for kv_append: cos in the first
+    half of the columns, sin in the second."""
+    device = torch.empty(0, device=device).device
+    with _Serving(device, stream) as s:
+        table = torch.empty(max_pos, rot_dim, dtype=torch.float32, device=device)
+        _check(load().saf_rope_table(_ptr(table), max_pos, rot_dim, base, s), "saf_rope_table")
+    return table
+
+
+def _strided(name: str, t: torch.Tensor, B: int, T: int, device):
+    """The (batch, head, token) strides of a [B, heads, T, 64] tensor, for the library."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.shape[0] != B or t.shape[2] != T or \
+            t.shape[3] != HEAD_DIM or t.stride(3) != 1:
+        raise ValueError(f"{name}: expected bf16 [{B}, heads, {T}, {HEAD_DIM}] with a contiguous last axis on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    st = t.stride()
+    # the stride of an axis of one entry is never used, and may be odd
+    return (ctypes.c_int64 * 3)(*(0 if t.shape[i] <= 1 else st[i] for i in range(3)))
+
+
+@_annotated
+def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
+              seq_lens: torch.Tensor, mask=None, q_lens: Optional[torch.Tensor] = None,
+              rope: Optional[torch.Tensor] = None, interleaved: bool = False, max_len: Optional[int] = None,
+              pos_offset: int = 0, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+              n_heads: Optional[int] = None, stream=None):
+    """Appends the new tokens k, v [B, H_kv, T, 64] to the cache and rotates q
+    [B, H, T, 64] (or None) and k by `rope` (a [len, rot_dim] table, or None) on
+    the way.  Returns (q_out, k_out).
+
+    The inputs may be strided (slices of one projection's output).  seq_lens
+    counts the cached tokens of each sequence including these; q_lens how many
+    of the T are new ones of the sequence (None: all).  mask: replaced heads
+    (their queries are skipped, and the keys of a K/V head that only they
+    read); without q it needs n_heads, the length of the mask.  Rows of q_out and
+    k_out that have no token or are skipped are left as they were (zeros where
+    this call allocates q_out).  k_out is written only if passed."""
+    B, Hkv, T, _ = k.shape
+    if mask is not None:
+        mask = head_mask(mask)
+    H = q.shape[1] if q is not None else n_heads if n_heads is not None else len(mask) if mask is not None else Hkv
+    device = kv.device
+    if Hkv != kv.h_kv:
+        raise ValueError(f"k has {Hkv} heads, the cache {kv.h_kv}")
+    if v.shape != k.shape:
+        raise ValueError("k and v differ in shape")
+    if mask is not None and len(mask) != H:
+        raise ValueError("mask length != H")
+    max_len = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
+    ks, vs = _strided("k", k, B, T, device), _strided("v", v, B, T, device)
+    qs = _strided("q", q, B, T, device) if q is not None else None
+    rope_len = rot_dim = 0
+    if rope is not None:
+        rope_len, rot_dim = rope.shape
+        _check_serving_tensors(device, [("rope", rope, torch.float32, (rope_len, rot_dim))])
+    if k_out is not None:
+        _check_serving_tensors(device, [("k_out", k_out, torch.bfloat16, (B, Hkv, T, HEAD_DIM))])
+    with _Serving(device, stream) as s:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.zeros(B, H, T, HEAD_DIM, dtype=torch.bfloat16, device=device)
+            else:
+                _check_serving_tensors(device, [("q_out", q_out, torch.bfloat16, (B, H, T, HEAD_DIM))])
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check(load().saf_kv_append(kv._addr, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out), _ptr(k_out),
+                                    _ptr(rope), rope_len, rot_dim, 1 if interleaved else 0, pos_offset, mask,
+                                    page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), _ptr(q_lens),
+                                    B, H, T, max_len, s), "saf_kv_append")
+    return q_out, k_out
+
+
+def paged_workspace_size(B: int, H: int, T_q: int, h_kv: int, prefix_len: int = 0) -> int:
+    """Workspace bytes of paged_attn (prefix_len 0) and paged_attn_prefix."""
+    n = load().saf_paged_workspace_size(B, H, h_kv, T_q, prefix_len)
+    if n == ctypes.c_size_t(-1).value:
+        raise SafError(SAF_ERR_INVALID_ARG, "saf_paged_workspace_size")
+    return int(n)
+
+
+def new_paged_workspace(kv: PagedKV, B: int, H: int, T_q: int = 1, prefix_len: int = 0) -> torch.Tensor:
+    """A zeroed workspace for the paged attention calls of up to these sizes."""
+    return torch.zeros(max(256, paged_workspace_size(B, H, T_q, kv.h_kv, prefix_len)), dtype=torch.uint8, device=kv.device)
+
+
+def _paged(q, kv, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
+           workspace, stream):
+    B, H, T, d = q.shape
+    device = kv.device
+    max_len = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
+    tensors = [("q", q, torch.bfloat16, (B, H, T, HEAD_DIM))]
+    if out is not None:
+        tensors.append(("out", out, torch.bfloat16, q.shape))
+    if lse is not None:
+        tensors.append(("lse", lse, torch.float32, (B, H, T)))
+    pattern_len = 0
+    if mask is not None:
+        mask = head_mask(mask)
+        if len(mask) != H:
+            raise ValueError("mask length != H")
+        if alpha is not None and rho is not None:
+            pattern_len = alpha.shape[-1]
+            tensors += [("alpha", alpha, torch.float32, (H, pattern_len)), ("rho", rho, torch.float32, (H, pattern_len))]
+        elif any(mask):
+            raise ValueError("replaced heads need alpha and rho")
+    if prefix_table is not None:
+        tensors.append(("prefix_table", prefix_table, torch.int32, (-(-prefix_len // kv.page_size),)))
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    _check_serving_tensors(device, tensors)
+    with _Serving(device, stream) as s:
+        # rows without a token are not written: they read as zeros where the call allocates
+        new = torch.empty if q_lens is None else torch.zeros
+        if out is None:
+            out = new(B, H, T, d, dtype=torch.bfloat16, device=device)
+        if lse is None:
+            lse = new(B, H, T, dtype=torch.float32, device=device)
+        if workspace is None:
+            workspace = new_paged_workspace(kv, B, H, T, prefix_len)
+        head = (kv._addr, q.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(alpha), _ptr(rho), pattern_len, mask)
+        tail = (page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), _ptr(q_lens), B, H, T, max_len,
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+        if prefix_table is None:
+            _check(load().saf_paged_attn(*head, *tail), "saf_paged_attn")
+        else:
+            _check(load().saf_paged_attn_prefix(*head, prefix_table.data_ptr(), prefix_len, *tail),
+                   "saf_paged_attn_prefix")
+    return out, lse
+
+
+@_annotated
+def paged_attn(q, kv: PagedKV, page_table, seq_lens, alpha=None, rho=None, mask=None, q_lens=None,
+               max_len: Optional[int] = None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of T new tokens per sequence, q [B, H, T, 64] (one token of a
+    decode step, a few drafted ones, a prompt chunk), over the cache that
+    already holds them.  Returns (O [B, H, T, 64] bf16, lse [B, H, T] fp32).
+
+    seq_lens [B], page_table [B, max_pages] int32 and q_lens (None, or [B] int32)
+    are device tensors, read by the kernels; max_len bounds the lengths.  mask,
+    alpha, rho: the replaced heads and their pattern ([H, pattern_len], at least
+    max_len long).  Callers that run many steps pass out, lse and a workspace
+    (new_paged_workspace)."""
+    return _paged(q, kv, None, 0, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
+                  workspace, stream)
+
+
+@_annotated
+def paged_attn_prefix(q, kv: PagedKV, prefix_table, prefix_len: int, page_table, seq_lens, alpha=None, rho=None,
+                      mask=None, q_lens=None, max_len: Optional[int] = None, out=None, lse=None, workspace=None,
+                      stream=None):
+    """paged_attn for a batch whose sequences all begin with the same
+    prefix_len tokens, cached once in the pages prefix_table [ceil(prefix_len /
+    page_size)]: the other arguments describe what follows the prefix."""
+    if prefix_len < 0:
+        raise ValueError("prefix_len < 0")
+    return _paged(q, kv, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask,
+                  q_lens, max_len, out, lse, workspace, stream)
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:
