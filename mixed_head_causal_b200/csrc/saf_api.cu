@@ -94,6 +94,18 @@ HeadBits head_bits(const uint8_t* mask, int H) {
     return hb;
 }
 
+// The K/V heads all of whose query heads are replaced: they keep no keys.
+HeadBits keyless_bits(const HeadBits& replaced, int H, int H_kv) {
+    HeadBits hb{};
+    const int group = H / H_kv;
+    for (int g = 0; g < H_kv; ++g) {
+        bool keyed = false;
+        for (int u = 0; u < group; ++u) keyed |= !replaced.get(g * group + u);
+        if (!keyed) hb.w[g >> 5] |= 1u << (g & 31);
+    }
+    return hb;
+}
+
 bool copy_strides(const int64_t* src, int64_t (&dst)[3]) {
     if (!src) return false;
     for (int i = 0; i < 3; ++i) {
@@ -399,12 +411,7 @@ saf_status saf_kv_append(const saf_paged_kv* kv, const void* q, const int64_t* q
     p.interleaved = interleaved ? 1 : 0;
     p.pos_offset = pos_offset;
     p.replaced = head_bits(replaced_mask, H);
-    const int group = H / kv->H_kv;
-    for (int g = 0; g < kv->H_kv; ++g) {
-        bool keyed = false;
-        for (int u = 0; u < group; ++u) keyed |= !p.replaced.get(g * group + u);
-        if (!keyed) p.keyless.w[g >> 5] |= 1u << (g & 31);
-    }
+    p.keyless = keyless_bits(p.replaced, H, kv->H_kv);
     p.page_table = page_table;
     p.seq_lens = seq_lens;
     p.q_lens = q_lens;
@@ -441,8 +448,9 @@ saf_status saf_paged_attn_prefix(const saf_paged_kv* kv, const void* q, void* o,
     if (prefix_len > 0 && !prefix_table) return SAF_ERR_INVALID_ARG;
     // positions, and rows of one K/V head over the batch, in 32 bits
     if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || (int64_t)B * H * T_q > INT_MAX / 128) return SAF_ERR_INVALID_ARG;
-    PagedParams p{};
+    PagedCall p{};
     p.replaced = head_bits(replaced_mask, H);
+    p.keyless = keyless_bits(p.replaced, H, kv->H_kv);
     bool any = false;
     for (uint32_t w : p.replaced.w) any |= w != 0;
     if (any) {

@@ -176,8 +176,7 @@ int sm_count();
 enum KernelId {
     KID_PATTERN = 1, KID_FWD_MMA = 2, KID_DOT = 3, KID_DKDV_MMA = 4, KID_DQ_MMA = 5,
     KID_FWD_TC = 6, KID_BWD_TC = 7, /* 8: retired */ KID_DQ_CONVERT = 9, KID_BWD_PRE = 10,
-    KID_GROUP_SUM = 11, KID_PATTERN_GRAD = 12, KID_CALIBRATION = 13, KID_FIT = 14,
-    KID_ROPE_TABLE = 15, KID_KV_APPEND = 16, KID_PAGED_ATTN = 17
+    KID_GROUP_SUM = 11, KID_PATTERN_GRAD = 12, KID_CALIBRATION = 13, KID_FIT = 14
 };
 // Every kernel launch of the library is bracketed by these two calls.
 void launch_begin(int kid, cudaStream_t s);
