@@ -359,45 +359,61 @@ def head_mask(mask) -> bytes:
     spares the serving calls the conversion."""
     if isinstance(mask, bytes):
         return mask
-    buf, n = _mask_buffer(mask)
-    return bytes(buf)[:n]
+    return bytes(1 if x else 0 for x in (mask.tolist() if isinstance(mask, torch.Tensor) else mask))
 
 
-def _check_serving_tensors(device, tensors) -> None:
-    """(name, tensor, dtype, shape) of each: contiguous, on `device`."""
-    for name, t, dtype, shape in tensors:
-        if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on {device}, "
-                             f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+def _refuse(name, t, dtype, shape, device):
+    raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on {device}, "
+                     f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _check_tables(kv, page_table, seq_lens, q_lens, B, max_len) -> int:
-    tables = [("page_table", page_table, torch.int32, (B, page_table.shape[-1])), ("seq_lens", seq_lens, torch.int32, (B,))]
-    if q_lens is not None:
-        tables.append(("q_lens", q_lens, torch.int32, (B,)))
-    _check_serving_tensors(kv.device, tables)
-    return page_table.shape[1] * kv.page_size if max_len is None else max_len
+def _check_serving(name, t, dtype, shape, device) -> int:
+    """The address of a tensor that is contiguous, of this type and shape, and on `device`.  (Written for
+    few attribute reads: a decode step's kernels take microseconds, and so do these checks.)"""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, device)
+    return t.data_ptr()
 
 
-class _Serving:
-    """The device and stream of a serving call: the cache's device is made
-    current, and what the call allocates belongs to the stream it runs on."""
+def _check_tables(kv, page_table, seq_lens, q_lens, B, max_len):
+    """(page_table, max_pages, seq_lens, q_lens, max_len) for the library."""
+    device, cols = kv.device, page_table.shape[-1]
+    return (_check_serving("page_table", page_table, torch.int32, (B, cols), device), cols,
+            _check_serving("seq_lens", seq_lens, torch.int32, (B,), device),
+            None if q_lens is None else _check_serving("q_lens", q_lens, torch.int32, (B,), device),
+            cols * kv.page_size if max_len is None else max_len)
+
+
+class _Guards:
+    """Makes a serving call's device and stream the current ones, so that what
+    it allocates belongs to the stream it runs on."""
 
     def __init__(self, device, stream):
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self._guards.append(torch.cuda.stream(stream))
+        self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
             g.__exit__(*exc)
+
+
+def _on_its_device(fn):
+    """A serving call under its cache's device and its stream argument (nothing to do when both are current)."""
+    @functools.wraps(fn)
+    def wrapper(kv, stream, *args):
+        if stream is None and kv.device.index == torch.cuda.current_device():
+            return fn(kv, *args)
+        with _Guards(kv.device, stream):
+            return fn(kv, *args)
+    return wrapper
+
+
+def _current_stream(device) -> int:
+    # torch.cuda.current_stream(device).cuda_stream, without its 3 us of wrapping
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 @_annotated
@@ -405,21 +421,24 @@ def rope_table(max_pos: int, rot_dim: int = HEAD_DIM, base: float = 10000.0, dev
     """Rotation table [max_pos, rot_dim] fp32 for kv_append: cos in the first
     half of the columns, sin in the second."""
     device = torch.empty(0, device=device).device
-    with _Serving(device, stream) as s:
+    with _Guards(device, stream):
         table = torch.empty(max_pos, rot_dim, dtype=torch.float32, device=device)
-        _check(load().saf_rope_table(_ptr(table), max_pos, rot_dim, base, s), "saf_rope_table")
+        _check(load().saf_rope_table(_ptr(table), max_pos, rot_dim, base, _current_stream(device)), "saf_rope_table")
     return table
 
 
-def _strided(name: str, t: torch.Tensor, B: int, T: int, device):
-    """The (batch, head, token) strides of a [B, heads, T, 64] tensor, for the library."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.shape[0] != B or t.shape[2] != T or \
-            t.shape[3] != HEAD_DIM or t.stride(3) != 1:
-        raise ValueError(f"{name}: expected bf16 [{B}, heads, {T}, {HEAD_DIM}] with a contiguous last axis on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+_Strides = ctypes.c_int64 * 3
+
+
+def _strided(name: str, t: torch.Tensor, shape, device):
+    """The (batch, head, token) strides of a bf16 tensor of this shape, for the library."""
     st = t.stride()
-    # the stride of an axis of one entry is never used, and may be odd
-    return (ctypes.c_int64 * 3)(*(0 if t.shape[i] <= 1 else st[i] for i in range(3)))
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device or st[3] != 1:
+        raise ValueError(f"{name}: expected bf16 of shape {tuple(shape)} with a contiguous last axis on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
+    if (st[0] | st[1] | st[2]) & 7:     # the stride of an axis of one entry is never used, and may be odd
+        st = [0 if n <= 1 else x for x, n in zip(st, shape)]
+    return _Strides(st[0], st[1], st[2])
 
 
 @_annotated
@@ -439,38 +458,39 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, kv: P
     read); without q it needs n_heads, the length of the mask.  Rows of q_out and
     k_out that have no token or are skipped are left as they were (zeros where
     this call allocates q_out).  k_out is written only if passed."""
+    H = q.shape[1] if q is not None else n_heads if n_heads is not None else len(mask) if mask is not None else k.shape[1]
+    return _kv_append(kv, stream, q, k, v, page_table, seq_lens, mask, q_lens, rope, interleaved, max_len, pos_offset,
+                      q_out, k_out, H)
+
+
+@_on_its_device
+def _kv_append(kv, q, k, v, page_table, seq_lens, mask, q_lens, rope, interleaved, max_len, pos_offset, q_out, k_out, H):
     B, Hkv, T, _ = k.shape
-    if mask is not None:
-        mask = head_mask(mask)
-    H = q.shape[1] if q is not None else n_heads if n_heads is not None else len(mask) if mask is not None else Hkv
     device = kv.device
     if Hkv != kv.h_kv:
         raise ValueError(f"k has {Hkv} heads, the cache {kv.h_kv}")
-    if v.shape != k.shape:
-        raise ValueError("k and v differ in shape")
-    if mask is not None and len(mask) != H:
-        raise ValueError("mask length != H")
-    max_len = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
-    ks, vs = _strided("k", k, B, T, device), _strided("v", v, B, T, device)
-    qs = _strided("q", q, B, T, device) if q is not None else None
-    rope_len = rot_dim = 0
-    if rope is not None:
-        rope_len, rot_dim = rope.shape
-        _check_serving_tensors(device, [("rope", rope, torch.float32, (rope_len, rot_dim))])
-    if k_out is not None:
-        _check_serving_tensors(device, [("k_out", k_out, torch.bfloat16, (B, Hkv, T, HEAD_DIM))])
-    with _Serving(device, stream) as s:
-        if q is not None:
-            if q_out is None:
-                q_out = torch.zeros(B, H, T, HEAD_DIM, dtype=torch.bfloat16, device=device)
-            else:
-                _check_serving_tensors(device, [("q_out", q_out, torch.bfloat16, (B, H, T, HEAD_DIM))])
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        _check(load().saf_kv_append(kv._addr, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_out), _ptr(k_out),
-                                    _ptr(rope), rope_len, rot_dim, 1 if interleaved else 0, pos_offset, mask,
-                                    page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), _ptr(q_lens),
-                                    B, H, T, max_len, s), "saf_kv_append")
+    if mask is not None:
+        mask = head_mask(mask)
+        if len(mask) != H:
+            raise ValueError("mask length != H")
+    table, cols, seq, ql, max_len = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
+    shape = (B, Hkv, T, HEAD_DIM)
+    ks, vs = _strided("k", k, shape, device), _strided("v", v, shape, device)
+    kop = None if k_out is None else _check_serving("k_out", k_out, torch.bfloat16, shape, device)
+    qp = qs = qop = None
+    if q is not None:
+        shape = (B, H, T, HEAD_DIM)
+        qp, qs = q.data_ptr(), _strided("q", q, shape, device)
+        if q_out is None:
+            q_out = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        qop = _check_serving("q_out", q_out, torch.bfloat16, shape, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope_len, rot_dim = (0, 0) if rope is None else rope.shape
+    rp = None if rope is None else _check_serving("rope", rope, torch.float32, (rope_len, rot_dim), device)
+    _check(load().saf_kv_append(kv._addr, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, qop, kop, rp, rope_len, rot_dim,
+                                1 if interleaved else 0, pos_offset, mask, table, cols, seq, ql, B, H, T, max_len,
+                                _current_stream(device)), "saf_kv_append")
     return q_out, k_out
 
 
@@ -487,48 +507,42 @@ def new_paged_workspace(kv: PagedKV, B: int, H: int, T_q: int = 1, prefix_len: i
     return torch.zeros(max(256, paged_workspace_size(B, H, T_q, kv.h_kv, prefix_len)), dtype=torch.uint8, device=kv.device)
 
 
-def _paged(q, kv, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
-           workspace, stream):
+@_on_its_device
+def _paged(kv, q, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse, workspace):
     B, H, T, d = q.shape
     device = kv.device
-    max_len = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
-    tensors = [("q", q, torch.bfloat16, (B, H, T, HEAD_DIM))]
-    if out is not None:
-        tensors.append(("out", out, torch.bfloat16, q.shape))
-    if lse is not None:
-        tensors.append(("lse", lse, torch.float32, (B, H, T)))
-    pattern_len = 0
+    shape = (B, H, T, HEAD_DIM)
+    qp = _check_serving("q", q, torch.bfloat16, shape, device)
+    tables = _check_tables(kv, page_table, seq_lens, q_lens, B, max_len)
+    pattern_len, ap, rp = 0, None, None
     if mask is not None:
         mask = head_mask(mask)
         if len(mask) != H:
             raise ValueError("mask length != H")
         if alpha is not None and rho is not None:
             pattern_len = alpha.shape[-1]
-            tensors += [("alpha", alpha, torch.float32, (H, pattern_len)), ("rho", rho, torch.float32, (H, pattern_len))]
+            ap = _check_serving("alpha", alpha, torch.float32, (H, pattern_len), device)
+            rp = _check_serving("rho", rho, torch.float32, (H, pattern_len), device)
         elif any(mask):
             raise ValueError("replaced heads need alpha and rho")
-    if prefix_table is not None:
-        tensors.append(("prefix_table", prefix_table, torch.int32, (-(-prefix_len // kv.page_size),)))
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+    # rows without a token are not written: they read as zeros where the call allocates
+    new = torch.empty if q_lens is None else torch.zeros
+    if out is None:
+        out = new(shape, dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = new((B, H, T), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = new_paged_workspace(kv, B, H, T, prefix_len)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {device}")
-    _check_serving_tensors(device, tensors)
-    with _Serving(device, stream) as s:
-        # rows without a token are not written: they read as zeros where the call allocates
-        new = torch.empty if q_lens is None else torch.zeros
-        if out is None:
-            out = new(B, H, T, d, dtype=torch.bfloat16, device=device)
-        if lse is None:
-            lse = new(B, H, T, dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = new_paged_workspace(kv, B, H, T, prefix_len)
-        head = (kv._addr, q.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr(alpha), _ptr(rho), pattern_len, mask)
-        tail = (page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), _ptr(q_lens), B, H, T, max_len,
-                workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
-        if prefix_table is None:
-            _check(load().saf_paged_attn(*head, *tail), "saf_paged_attn")
-        else:
-            _check(load().saf_paged_attn_prefix(*head, prefix_table.data_ptr(), prefix_len, *tail),
-                   "saf_paged_attn_prefix")
+    head = (kv._addr, qp, _check_serving("out", out, torch.bfloat16, shape, device),
+            _check_serving("lse", lse, torch.float32, (B, H, T), device), ap, rp, pattern_len, mask)
+    tail = (*tables[:4], B, H, T, tables[4], workspace.data_ptr(), workspace.nbytes, _current_stream(device))
+    if prefix_table is None:
+        _check(load().saf_paged_attn(*head, *tail), "saf_paged_attn")
+    else:
+        pages = _check_serving("prefix_table", prefix_table, torch.int32, (-(-prefix_len // kv.page_size),), device)
+        _check(load().saf_paged_attn_prefix(*head, pages, prefix_len, *tail), "saf_paged_attn_prefix")
     return out, lse
 
 
@@ -544,8 +558,7 @@ def paged_attn(q, kv: PagedKV, page_table, seq_lens, alpha=None, rho=None, mask=
     alpha, rho: the replaced heads and their pattern ([H, pattern_len], at least
     max_len long).  Callers that run many steps pass out, lse and a workspace
     (new_paged_workspace)."""
-    return _paged(q, kv, None, 0, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
-                  workspace, stream)
+    return _paged(kv, stream, q, None, 0, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse, workspace)
 
 
 @_annotated
@@ -557,8 +570,8 @@ def paged_attn_prefix(q, kv: PagedKV, prefix_table, prefix_len: int, page_table,
     page_size)]: the other arguments describe what follows the prefix."""
     if prefix_len < 0:
         raise ValueError("prefix_len < 0")
-    return _paged(q, kv, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask,
-                  q_lens, max_len, out, lse, workspace, stream)
+    return _paged(kv, stream, q, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
+                  workspace)
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:
