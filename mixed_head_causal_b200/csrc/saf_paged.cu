@@ -2,28 +2,36 @@
 //
 // Work is a list of items (sequence b, K/V head g, row block): the rows of one
 // item are the G = H / H_kv query heads of the group times the T new tokens,
-// and share every key.  Keys come in tiles of 64.  The tiles of all items form
-// one axis, weighted by the bytes they read (2 with K and V, 1 for a K/V head
-// whose query heads are all replaced, which has no keys), and each CTA of a
-// grid that fills the GPU takes an equal stretch of it, wherever that begins
-// and ends: lengths are read on the device, so a captured call follows them.
-// An item that one CTA holds whole is written at once; the others leave
-// (m, l, O) pieces in the workspace, and the CTA that finishes an item's last
-// piece joins them in key order (the result does not depend on which CTA that is).
+// and share every key.  Keys come in tiles of 16 KB: 64 keys with K and V, or 128
+// of V alone for a K/V head whose query heads are all replaced (it has no
+// keys).  The tiles of all items form one axis, and each CTA of a grid that
+// fills the GPU takes an equal stretch of it: lengths are read on the device,
+// so a captured call follows them.  An item that one CTA holds whole is written
+// at once; the others leave (m, l, O) pieces in the workspace, and the CTA that
+// finishes an item's last piece joins them in key order (the result does not
+// depend on which CTA that is).  An item costs a CTA about 2 us besides its
+// tiles, and joining pieces 3 us of round trips, each a few tiles' worth of
+// reading: an item begins with kItem units on the axis that stand for no tile, a CTA
+// gets at least kMinUnits, and a stretch that would end within kSnap units of an
+// item's ends ends there.
 //
-// A CTA is one producer warp and four consumer warps.  The producer looks up
-// the pages of a tile and fetches them by TMA (128-byte swizzle) into a ring;
-// a tile of 64 keys is 64 / page_size boxes.  The consumers split the tile's
-// keys (and, above 16 rows, the rows): S = Q K^T and O += P V as warp-level
-// m16n8k16 MMAs with a running maximum and sum per row and warp,
+// A CTA is one producer warp and four or eight consumer warps.  The producer
+// walks the items ahead of the others, works out their rows, fetches their
+// queries, looks up the pages of a tile and fetches them by TMA (128-byte swizzle)
+// into a ring, a box per page (64 rows at most).  The consumer warps take 64 keys
+// in turn (a tile of V alone goes to two of them), so that one warp's chain of
+// MMA, maximum, exponentials, MMA overlaps the others'.  The few rows are the N
+// side of the warp-level m16n8k16 MMAs, eight to a block, and the keys (then the
+// 64 columns of V) the M side:
+//   S^T = K Q^T                    (M keys, N rows), a running maximum m and sum l per row
 //   ordinary row   s = q . k / 8
 //   replaced row   s = a[j] + r[i - j]      (Eq. (3): its softmax is the pattern)
-// joined over the warps at the end of an item.
+//   O^T += V^T P^T                 (M columns, N rows), P = exp(s - m) as bf16
+// The warps' (m, l, O) are joined at the end of an item.
 //
 // One new token makes this a stream of K and V at a few flops per byte: HBM
-// bounds it, so the warp-level MMAs (a tile of 16 rows costs about 130 of the
-// 700 cycles in which HBM delivers it to one SM) are enough, and the kernel is
-// built for bytes in flight.
+// bounds it, so the warp-level MMAs are enough, and the kernel is built for bytes
+// in flight and short chains.
 #include <limits.h>
 
 #include <algorithm>
@@ -35,25 +43,67 @@ namespace saf {
 namespace {
 
 using namespace tc;
-using mma::load_b_frag_kn;
-using mma::load_b_frag_nk;
 using mma::mma_bf16;
 
-constexpr int TK = 64;               // keys per tile
-constexpr int NS = 3;                // ring stages
-constexpr int NCONS = 128;           // consumer threads (four warps), then the producer warp
-constexpr int CTAS_PER_SM = 3;
+constexpr int TK = 64;               // keys per tile with K and V (twice as many of V alone)
+constexpr int CTAS_PER_SM = 2;
 constexpr int kMaxGrid = 1024;       // bounds the workspace
+constexpr int kItem = 4, kSnap = 4, kMinUnits = 8;
+constexpr int kMaxBlocks = 4;        // row blocks of eight that one item holds
 constexpr uint32_t HALF = TK * 128;  // bytes of a tile's K or V
 constexpr uint32_t STAGE = 2 * HALF;
-constexpr int RED_PITCH = 72;        // floats per row of a warp's O: eight-byte stores of a quad row hit distinct banks
-constexpr uint32_t SM_RED = NS * STAGE;
-constexpr uint32_t SM_ML = SM_RED + 4 * 16 * RED_PITCH * 4;  // [4 warps][16 rows] m, then l
-constexpr uint32_t SM_BAR = SM_ML + 2 * 4 * 16 * 4;
-constexpr uint32_t SM_INFO = SM_BAR + 16 * NS;  // [NS] pages of a stage that are none; the scan's sums and results
-constexpr uint32_t SM_TOTAL = SM_INFO + 4 * NS + 4 * 8;
-constexpr uint32_t SM_ALLOC = SM_TOTAL + 1024;  // the ring starts on a 1024-byte boundary (swizzle atoms)
+constexpr int RED_PITCH = 68;        // floats per row of a warp's O: a warp's stores hit distinct banks
+constexpr int Q_PITCH = 144;         // bytes per query row in shared memory: eight rows' words hit distinct banks
 constexpr long long kWaitLimit = 1ll << 31;
+
+// What the consumers need of an item's stretch: tiles [t0, t1), pieces of the
+// item in all, the CTA of its first one; vmin: keys that every row sees; replaced:
+// bit per row (those that see a key).
+struct Piece {
+    int len, keyed, t0, t1, pieces, c_first, rows, vmin;
+    uint32_t replaced;
+};
+// One row of an item.  A replaced row looks its scores up: a at local key j is
+// a[a0 + j], r is r[r0 - j], for j < vis.
+struct RowInfo {
+    long long a0, r0;
+    int vis;        // keys it sees
+    int out, part;  // its row of the output (-1: it has no token), and of the prefix's parts
+    int replaced;
+};
+
+// Shared memory of a CTA whose items hold up to 8 NB rows, two CTAs to an SM.
+template <int NB>
+struct Smem {
+    static constexpr int ROWS = 8 * NB;
+    static constexpr int NCW = NB == 1 ? 8 : 4;                     // consumer warps (their registers: see KC)
+    static constexpr int NS = NB <= 2 ? 5 : NB == 3 ? 4 : 3;        // ring stages
+    static constexpr int NI = NB <= 2 ? 4 : 3;                      // items under way
+    static constexpr int KC = NB <= 2 ? 64 : 32;                    // keys whose scores a warp holds at a time
+    static constexpr uint32_t RED = NS * STAGE;                     // [NCW][ROWS][RED_PITCH] O of a warp
+    static constexpr uint32_t ML = RED + NCW * ROWS * RED_PITCH * 4;  // [NCW][ROWS] m, then l
+    static constexpr uint32_t ITEM = ML + 2 * NCW * ROWS * 4;       // [NI] Piece
+    static constexpr uint32_t INFO = ITEM + NI * 48;                // [NI][ROWS] RowInfo
+    static constexpr uint32_t Q = INFO + NI * ROWS * sizeof(RowInfo);  // [NI][ROWS][Q_PITCH]
+    static constexpr uint32_t BAR = Q + NI * ROWS * Q_PITCH;        // ring full, empty; item full, free; join
+    static constexpr uint32_t META = BAR + 16 * NS + 16 * NI + 8;   // [NS] boxes of a stage without a page; tiles issued; last
+    static constexpr uint32_t TOTAL = META + 4 * NS + 8 + 1024;     // the ring starts on a 1024-byte boundary
+};
+static_assert(sizeof(Piece) <= 48 && sizeof(RowInfo) == 32, "shared memory slots");
+
+// Division by a launch constant: n / d = (umulhi(n, m) + n) >> s for 0 <= n < 2^31, with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1 (the round-up method of Granlund and Montgomery).  A few cycles, where the
+// general division's code, cold at the start of a launch, costs hundreds.
+struct Divisor {
+    uint32_t m, s;
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+};
+inline Divisor divisor(int d) {
+    Divisor x{0, 0};
+    while ((1ll << x.s) < d) ++x.s;
+    x.m = (uint32_t)(((1ull << 32) * ((1ull << x.s) - (uint64_t)d)) / (uint64_t)d + 1);
+    return x;
+}
 
 struct SplitParams {
     const __nv_bfloat16* q;
@@ -61,13 +111,14 @@ struct SplitParams {
     float* lse;
     const float *a, *r;
     int pattern_len, prefix_len;
-    HeadBits replaced, keyless;
+    HeadBits replaced;
     const int32_t *table, *seq_lens, *q_lens;
     int table_stride, num_pages, log_page, Hkv;
     int B, H, T, G, R, max_len;  // R = G T rows of one (b, g)
     int nseq, rows, nrb;         // key sequences, rows of one item list entry, row blocks
-    int wsum;                    // sum of the K/V heads' weights
-    uint8_t g_of_w[2 * kMaxHeads];  // K/V head of each weight unit
+    Divisor by_T, by_R, by_nrb;
+    int keyed;                   // K/V heads with keys: the first of order[]
+    uint8_t order[kMaxHeads];    // K/V heads, those with keys first
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
     float* part;                 // [Hkv * B * R][64] O, then [Hkv * B * R] m, then l, of the prefix (or null)
@@ -86,456 +137,619 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n) : "memory");
+}
+// A packed 8 x 8 matrix of 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
 
 // exp(x - m) for finite or -inf x <= m (m = -inf: no weight yet).
 __device__ __forceinline__ float weight(float x, float m) { return ex2((x - (m == kNegInf ? 0.f : m)) * kLog2e); }
-
-// A stretch [lo, hi) of the weighted tile axis, walked item by item.  The axis
-// runs over sequences, their K/V heads, row blocks and tiles; a tile belongs to
-// the CTA whose stretch holds its first unit.
-struct Piece {
-    int b, g, rb, t0, t1, n, len, w;  // tiles [t0, t1) of the item's n; len keys
-    long long start;                  // unit of the item's tile 0
-};
-struct Walk {
-    long long u, hi, base;  // next unit, end, first unit of sequence b
-    int b, len, tiles;
-};
 
 template <bool PREFIX>
 __device__ __forceinline__ int key_len(const SplitParams& p, int b) {
     return PREFIX ? p.prefix_len : min(max(p.seq_lens[b], 0), p.max_len);
 }
-// An item without keys still takes one (empty) tile: its rows are written.
-__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + TK - 1) / TK); }
-
-template <bool PREFIX>
-__device__ __forceinline__ bool next_piece(const SplitParams& p, Walk& w, Piece& x) {
-    while (w.u < w.hi && w.b < p.nseq) {
-        const int block = w.tiles * p.nrb;  // tiles of one weight unit
-        const int off = (int)(w.u - w.base);
-        if (off >= block * p.wsum) {
-            w.base += (long long)block * p.wsum;
-            if (++w.b < p.nseq) {
-                w.len = key_len<PREFIX>(p, w.b);
-                w.tiles = tiles_of(w.len);
-            }
-            continue;
-        }
-        int gw = off / block;
-        x.g = p.g_of_w[gw];
-        if (gw > 0 && p.g_of_w[gw - 1] == x.g) --gw;
-        x.w = p.keyless.get(x.g) ? 1 : 2;
-        const int in_g = off - gw * block, item = w.tiles * x.w;
-        x.rb = in_g / item;
-        const int in_item = in_g - x.rb * item;
-        x.start = w.u - in_item;
-        x.t0 = (in_item + x.w - 1) / x.w;
-        x.t1 = (int)min((long long)w.tiles, (w.hi - x.start + x.w - 1) / x.w);
-        x.b = w.b;
-        x.n = w.tiles;
-        x.len = w.len;
-        w.u = x.start + item;
-        if (x.t0 < x.t1) return true;
-    }
-    return false;
+__device__ __forceinline__ int new_tokens(const SplitParams& p, int b) {
+    return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+}
+// Tiles of an item (one without keys still takes one, empty, tile: its rows are written).
+__device__ __forceinline__ int tiles_of(int len, bool keyed) {
+    const int tk = keyed ? TK : 2 * TK;
+    return max(1, (len + tk - 1) / tk);
+}
+// Units of a sequence on the axis.
+__device__ __forceinline__ int seq_units(const SplitParams& p, int len) {
+    return p.nrb * (p.keyed * (tiles_of(len, true) + kItem) + (p.Hkv - p.keyed) * (tiles_of(len, false) + kItem));
 }
 
-// One row of an item: rr counts the rows of the item list entry.
-struct Row {
-    int b, h, t;  // sequence, query head, new token
-    int pos;      // position of the row, the prefix included
-    bool valid;
+// The item that unit u of sequence b is in (base: the sequence's first unit).
+struct Item {
+    int gi, rb, n, start;  // its tiles, its first unit
+    bool keyed;
 };
-template <bool PREFIX>
-__device__ __forceinline__ Row row_of(const SplitParams& p, int b, int g, int rr) {
-    Row x;
-    x.b = PREFIX ? rr / p.R : b;
-    const int rem = PREFIX ? rr - x.b * p.R : rr;
-    x.valid = rr < p.rows;
-    if (!x.valid) {
-        x.b = x.h = x.t = x.pos = 0;
-        return x;
+__device__ __forceinline__ Item item_at(const SplitParams& p, int base, int len, int u) {
+    Item x;
+    int off = u - base;
+    x.n = tiles_of(len, true);
+    const int keyed_units = p.keyed * p.nrb * (x.n + kItem);
+    x.keyed = off < keyed_units;
+    int first = 0;
+    if (!x.keyed) {
+        x.n = tiles_of(len, false);
+        off -= keyed_units;
+        first = p.keyed;
     }
-    const int u = rem / p.T;
-    x.h = g * p.G + u;
-    x.t = rem - u * p.T;
-    const int n = p.q_lens ? min(max(p.q_lens[x.b], 0), p.T) : p.T;
-    x.valid = x.t < n;
-    x.pos = p.prefix_len + key_len<false>(p, x.b) - n + x.t;
+    const int block = (int)((unsigned)off / (unsigned)(x.n + kItem));  // K/V head and row block
+    x.gi = p.by_nrb.div(block);
+    x.rb = block - x.gi * p.nrb;
+    x.gi += first;
+    x.start = u - (off - block * (x.n + kItem));
+    return x;
+}
+
+// Row rr of the item list entry (b, g); n, pos0: the sequence's new tokens and
+// the position of the first (with PREFIX they are looked up per row).
+template <bool PREFIX>
+__device__ __forceinline__ RowInfo row_info(const SplitParams& p, int b, int g, int len, int n, int pos0, int rr) {
+    RowInfo x;
+    x.a0 = x.r0 = 0;
+    x.vis = x.part = 0;
+    x.out = -1;
+    x.replaced = 0;
+    if (rr >= p.rows) return x;
+    const int rb = PREFIX ? p.by_R.div(rr) : b, rem = PREFIX ? rr - rb * p.R : rr;
+    const int u = p.by_T.div(rem), h = g * p.G + u, t = rem - u * p.T;
+    if (PREFIX) {
+        n = new_tokens(p, rb);
+        pos0 = p.prefix_len + key_len<false>(p, rb) - n;
+    }
+    if (t >= n) return x;
+    const int key_base = PREFIX ? 0 : p.prefix_len;  // position of local key 0
+    const long long ph = (long long)h * p.pattern_len;
+    x.vis = max(0, min(len, pos0 + t - key_base + 1));
+    x.a0 = ph + key_base;
+    x.r0 = ph + pos0 + t - key_base;
+    x.out = (rb * p.H + h) * p.T + t;
+    x.part = (g * p.B + rb) * p.R + rem;
+    x.replaced = p.replaced.get(h);
     return x;
 }
 
 // A finished row (four columns from c): with PREFIX the part that the batch's
 // own keys are joined to, else the output, after joining the prefix's part.
 template <bool PREFIX>
-__device__ __forceinline__ void finish_row(const SplitParams& p, int b, int g, int rr, int c, float4 o, float m, float l) {
-    const Row x = row_of<PREFIX>(p, b, g, rr);
-    if (!x.valid) return;
+__device__ __forceinline__ void finish_row(const SplitParams& p, const RowInfo& x, int c, float4 o, float m, float l) {
+    if (x.out < 0) return;
     const size_t nrow = (size_t)p.Hkv * p.B * p.R;
-    const size_t pr = ((size_t)g * p.B + x.b) * p.R + (x.h - g * p.G) * p.T + x.t;
+    float* part = p.part + (size_t)x.part * kHeadDim + c;
+    float* part_m = p.part + nrow * kHeadDim + x.part;
     if (PREFIX) {
-        *reinterpret_cast<float4*>(p.part + pr * kHeadDim + c) = o;
+        *reinterpret_cast<float4*>(part) = o;
         if (c == 0) {
-            p.part[nrow * kHeadDim + pr] = m;
-            p.part[nrow * (kHeadDim + 1) + pr] = l;
+            part_m[0] = m;
+            part_m[nrow] = l;
         }
         return;
     }
     if (p.part) {
-        const float4 o2 = __ldcg(reinterpret_cast<const float4*>(p.part + pr * kHeadDim + c));
-        const float m2 = __ldcg(p.part + nrow * kHeadDim + pr), l2 = __ldcg(p.part + nrow * (kHeadDim + 1) + pr);
+        const float4 o2 = __ldcg(reinterpret_cast<const float4*>(part));
+        const float m2 = __ldcg(part_m), l2 = __ldcg(part_m + nrow);
         const float mm = fmaxf(m, m2), f = weight(m, mm), f2 = weight(m2, mm);
         o = make_float4(o.x * f + o2.x * f2, o.y * f + o2.y * f2, o.z * f + o2.z * f2, o.w * f + o2.w * f2);
         l = l * f + l2 * f2;
         m = mm;
     }
-    const size_t row = ((size_t)x.b * p.H + x.h) * p.T + x.t;
     const bool some = !(l == 0.f);  // also a NaN
-    const float s = some ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(p.o + row * kHeadDim + c) = make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
-    if (c == 0) p.lse[row] = some ? m + logf(l) : kNegInf;
+    const float s = some ? __fdividef(1.f, l) : 0.f;
+    *reinterpret_cast<uint2*>(p.o + (size_t)x.out * kHeadDim + c) =
+        make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
+    if (c == 0) p.lse[x.out] = some ? m + __logf(l) : kNegInf;
 }
 
-// WR warps split the rows (16 each), WK = 4 / WR the keys of a tile.
-template <int WR, bool PREFIX>
-__global__ void __launch_bounds__(NCONS + 32, CTAS_PER_SM)
+template <int NB, bool PREFIX>
+__global__ void __launch_bounds__(32 * (Smem<NB>::NCW + 1), CTAS_PER_SM)
 paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ SplitParams p) {
-    constexpr int WK = 4 / WR, KW = TK / WK, NT = KW / 8, RT = 16 * WR;
-    constexpr int SLOT = RT * (kHeadDim + 2);
+    using L = Smem<NB>;
+    constexpr int ROWS = L::ROWS, NCW = L::NCW, NS = L::NS, NI = L::NI, KB = L::KC / 16, NCONS = 32 * NCW;
+    // P as one bf16 (half a step of 2^-8 off, as in the layer's own forward), or as a hi + lo pair of 16 bits where
+    // the second product is free: with up to eight rows the stream of K and V leaves the tensor pipe the room.
+    constexpr bool SPLIT_P = NB == 1;
+    constexpr int SLOT = ROWS * (kHeadDim + 2);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t bar_full = sbase + SM_BAR, bar_empty = bar_full + 8 * NS;
-    uint32_t* meta = reinterpret_cast<uint32_t*>(smem + SM_INFO);
-    int* scan_sums = reinterpret_cast<int*>(smem + SM_INFO) + NS;  // [5]
-    int* first = scan_sums + 5;  // the stretch's first sequence, and the tiles before it
-    int* last_flag = first + 2;
+    const uint32_t bar_full = sbase + L::BAR, bar_empty = bar_full + 8 * NS;
+    const uint32_t bar_item = bar_empty + 8 * NS, bar_taken = bar_item + 8 * NI, bar_join = bar_taken + 8 * NI;
+    uint32_t* meta = reinterpret_cast<uint32_t*>(smem + L::META);
+    volatile int* issued = reinterpret_cast<int*>(smem + L::META) + NS;  // tiles whose loads the producer has issued
+    volatile int* last_flag = issued + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 4);
+            mbar_init(bar_empty + 8 * s, 2);
         }
+        for (int s = 0; s < NI; ++s) {
+            mbar_init(bar_item + 8 * s, 1);
+            mbar_init(bar_taken + 8 * s, NCW);
+        }
+        mbar_init(bar_join, NCW);
+        *issued = 0;
         fence_mbar_init();
-    }
-    // ---- this CTA's stretch: each thread sums the tiles of a run of sequences
-    constexpr int NTH = NCONS + 32;
-    const int chunk = (p.nseq + NTH - 1) / NTH, b_lo = min(tid * chunk, p.nseq), b_hi = min(b_lo + chunk, p.nseq);
-    int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(key_len<PREFIX>(p, b));
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) scan_sums[warp] = incl;
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int k = 0; k < NTH / 32; ++k) {
-        if (k < warp) before += scan_sums[k];
-        total += scan_sums[k];
-    }
-    const long long per_tile = (long long)p.nrb * p.wsum;
-    const long long units = total * per_tile;
-    // at least two units per CTA: then every stretch inside an item holds a tile
-    const long long ctas = max(1ll, min((long long)gridDim.x, units / 2));
-    if (blockIdx.x >= ctas) return;
-    const long long lo = blockIdx.x * units / ctas, hi = (blockIdx.x + 1) * units / ctas;
-    {
-        long long at = before + incl - mine;  // tiles before this thread's run
-        if (lo >= at * per_tile && lo < (at + mine) * per_tile) {
-            int b = b_lo;
-            for (; b < b_hi; ++b) {
-                const int t = tiles_of(key_len<PREFIX>(p, b));
-                if (lo < (at + t) * per_tile) break;
-                at += t;
-            }
-            first[0] = b;
-            first[1] = (int)at;
-        }
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
     }
     __syncthreads();
     if (PREFIX) griddep_launch_dependents();  // the batch's own keys may start
-    Walk wk;
-    wk.u = lo;
-    wk.hi = hi;
-    wk.b = first[0];
-    wk.base = first[1] * per_tile;
-    wk.len = key_len<PREFIX>(p, wk.b);
-    wk.tiles = tiles_of(wk.len);
-    auto cta_of = [&](long long u) { return (int)(((u + 1) * ctas - 1) / units); };
-    Piece x;
 
-    if (warp == NCONS / 32) {
+    if (warp == NCW) {
         // ------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tmap(&tmK);
-            prefetch_tmap(&tmV);
+        // The CTA's stretch: each lane sums the units of a run of sequences.
+        const int chunk = (p.nseq + 31) >> 5, b_lo = min(lane * chunk, p.nseq), b_hi = min(b_lo + chunk, p.nseq);
+        int mine = 0;
+#pragma unroll 4
+        for (int b = b_lo; b < b_hi; ++b) mine += seq_units(p, key_len<PREFIX>(p, b));
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += v;
         }
-        const int lp = p.log_page;
-        const int boxes = max(1, TK >> lp);
-        const uint32_t box_bytes = (uint32_t)min(TK, 1 << lp) * 128;
+        const int total = __shfl_sync(~0u, incl, 31), before = incl - mine;
+        // Stretch c begins at unit c * per + min(c, more): `more` stretches of per + 1 units, then those of `per`.
+        const int ctas = max(1, min((int)gridDim.x, total / kMinUnits)), cta = blockIdx.x;
+        const int per = (int)((unsigned)total / (unsigned)ctas), more = total - per * ctas;
+        const int lo = cta < ctas ? cta * per + min(cta, more) : total, hi = lo + per + (cta < more ? 1 : 0);
+        // The sequence of a unit below `total`, and its first unit.
+        auto find = [&](int u, int& b, int& base) {
+            const int src = __ffs(__ballot_sync(~0u, u >= before && u < before + mine)) - 1;
+            int at = before, bb = b_lo;
+            if (lane == src)
+                for (;; ++bb) {
+                    const int n = seq_units(p, key_len<PREFIX>(p, bb));
+                    if (u < at + n) break;
+                    at += n;
+                }
+            b = __shfl_sync(~0u, bb, src);
+            base = __shfl_sync(~0u, at, src);
+        };
+        int b = 0, base = 0, b_end = 0, base_end = 0;
+        if (lo < total) find(lo, b, base);
+        if (lo < total && hi < total) find(hi, b_end, base_end);
+        int len = key_len<PREFIX>(p, b);
+        // stretch ends close to an item's end move there
+        auto snapped = [&](int u, int bu, int base_u) {
+            const Item x = item_at(p, base_u, key_len<PREFIX>(p, bu), u);
+            const int stop = x.start + kItem + x.n;
+            return u - x.start <= kItem + kSnap ? x.start : stop - u <= kSnap ? stop : u;
+        };
+        int u = lo < total ? snapped(lo, b, base) : total;
+        const int end = hi < total ? snapped(hi, b_end, base_end) : total;
+        // The first stretch that begins at unit x > 0 or later.
+        auto first_from = [&](int x) {
+            const int big = more * (per + 1);
+            return x <= big ? (int)((unsigned)(x + per) / (unsigned)(per + 1))
+                            : more + (int)((unsigned)(x - big + per - 1) / (unsigned)per);
+        };
+        const int lp = p.log_page, lb = min(lp, 6);  // page and box rows
+        const uint32_t box_bytes = 128u << lb;
         int it = 0;
-        bool ok = true;
-        while (ok && next_piece<PREFIX>(p, wk, x)) {
-            const bool keys = x.w == 2;
-            const int32_t* table = p.table + (size_t)x.b * p.table_stride;
+        // a wait gave up: the loads in flight land (or give up in turn) before the shared memory is let go
+        auto give_up = [&](unsigned code) {
+            if (lane == 0) {
+                report(p.err, code);
+                for (int k = max(0, it - NS); k < it; ++k) mbar_wait(bar_full + 8 * (k % NS), (k / NS) & 1, kWaitLimit);
+            }
+        };
+        for (int ni = 0;; ++ni) {
+            Piece x;
+            Item w;
+            x.t1 = -1;  // no more
+            if (u < end) {
+                while (u >= base + seq_units(p, len)) {
+                    base += seq_units(p, len);
+                    len = key_len<PREFIX>(p, ++b);
+                }
+                w = item_at(p, base, len, u);
+                x.len = len;
+                x.keyed = w.keyed;
+                x.t0 = max(0, u - w.start - kItem);
+                x.t1 = min(w.n, end - w.start - kItem);
+                // the stretches that begin strictly inside the item (see snapped())
+                const int in_lo = w.start + kItem + kSnap + 1, in_hi = w.start + kItem + w.n - kSnap;
+                const int c1 = in_lo < in_hi ? first_from(in_lo) : 0, c2 = in_lo < in_hi ? first_from(in_hi) : 0;
+                x.pieces = c2 - c1 + 1;
+                x.c_first = c1 - 1;
+                u = w.start + kItem + x.t1;
+            }
+            const int slot = ni % NI;
+            if (!mbar_wait_warp(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1, kWaitLimit)) {
+                give_up(0x403);
+                return;
+            }
+            if (x.t1 < 0) {
+                if (lane == 0) {
+                    reinterpret_cast<Piece*>(smem + L::ITEM + 48 * slot)->t1 = -1;
+                    mbar_arrive(bar_item + 8 * slot);
+                }
+                return;
+            }
+            const int g = p.order[w.gi], row0 = w.rb * ROWS;
+            x.rows = min(ROWS, p.rows - row0);
+            {  // a lane per row
+                const int n = PREFIX ? 0 : new_tokens(p, b);
+                const RowInfo row = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, row0 + lane);
+                x.replaced = __ballot_sync(~0u, lane < x.rows && row.replaced && row.vis > 0);
+                x.vmin = __reduce_min_sync(~0u, lane < x.rows && row.out >= 0 ? row.vis : INT_MAX);
+                if (lane < ROWS) *reinterpret_cast<RowInfo*>(smem + L::INFO + (slot * ROWS + lane) * sizeof(RowInfo)) = row;
+            }
+            if (lane == 0) *reinterpret_cast<Piece*>(smem + L::ITEM + 48 * slot) = x;
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(bar_item + 8 * slot, x.rows * 128);
+            __syncwarp();
+            if (lane < x.rows) {  // the queries
+                const int rr = row0 + lane, qb = PREFIX ? p.by_R.div(rr) : b, rem = PREFIX ? rr - qb * p.R : rr;
+                bulk_load(sbase + L::Q + (slot * ROWS + lane) * Q_PITCH,
+                          p.q + (((size_t)qb * p.H + g * p.G) * p.T + rem) * kHeadDim, 128, bar_item + 8 * slot);
+            }
+            const int tk = w.keyed ? TK : 2 * TK, boxes = tk >> lb;
+            const int32_t* table = p.table + (size_t)b * p.table_stride;
             const int npages = (x.len + (1 << lp) - 1) >> lp;
             int ids = -1, ids0 = -64;  // page ids [ids0, ids0 + 32), one per lane
             for (int t = x.t0; t < x.t1; ++t, ++it) {
-                const int s = it % NS, pg0 = (t * TK) >> lp;
-                if (pg0 >= ids0 + 32 || pg0 < ids0) {
-                    ids0 = pg0;
-                    ids = pg0 + lane < npages ? __ldg(table + pg0 + lane) : -1;
+                const int s = it % NS, key = t * tk + (lane << lb);  // this lane's box
+                const int pg_lo = (t * tk) >> lp, pg_hi = (t * tk + tk - 1) >> lp;
+                if (pg_lo < ids0 || pg_hi >= ids0 + 32) {
+                    ids0 = pg_lo;
+                    ids = pg_lo + lane < npages ? __ldg(table + pg_lo + lane) : -1;
                 }
-                const int page = __shfl_sync(~0u, ids, (pg0 - ids0 + lane) & 31);
-                const bool need = lane < boxes && pg0 + lane < npages;
+                const int page = __shfl_sync(~0u, ids, ((key >> lp) - ids0) & 31);
+                const bool need = lane < boxes && key < x.len;
                 const bool good = need && page >= 0 && page < p.num_pages;
                 const uint32_t bad = __ballot_sync(~0u, need && !good);
                 const int loads = __popc(__ballot_sync(~0u, good));
-                ok = mbar_wait_warp(bar_empty + 8 * s, ((it / NS) & 1) ^ 1, kWaitLimit);
-                if (!ok) {
-                    if (lane == 0) report(p.err, 0x401);
-                    break;
+                if (!mbar_wait_warp(bar_empty + 8 * s, ((it / NS) & 1) ^ 1, kWaitLimit)) {
+                    give_up(0x401);
+                    return;
                 }
                 if (lane == 0) {
                     meta[s] = bad;
-                    mbar_expect_tx(bar_full + 8 * s, loads * box_bytes * (keys ? 2 : 1));
+                    mbar_expect_tx(bar_full + 8 * s, loads * box_bytes * (w.keyed ? 2 : 1));
                 }
                 __syncwarp();
                 if (good) {
                     const uint32_t dst = sbase + s * STAGE + lane * box_bytes;
-                    const int y = (t * TK) & ((1 << lp) - 1);
-                    if (keys) tma_load_4d(dst, &tmK, bar_full + 8 * s, 0, y, x.g, page);
-                    tma_load_4d(dst + HALF, &tmV, bar_full + 8 * s, 0, y, x.g, page);
+                    const int y = key & ((1 << lp) - 1);
+                    if (w.keyed) tma_load_4d(dst, &tmK, bar_full + 8 * s, 0, y, g, page);
+                    tma_load_4d(dst + (w.keyed ? HALF : 0), &tmV, bar_full + 8 * s, 0, y, g, page);
                 }
+                if (lane == 0) *issued = it + 1;
             }
         }
-        return;
     }
 
     // ---------------------------------------------------- consumers
-    const int wr = warp / WK, wkey = warp % WK;
-    float* red = reinterpret_cast<float*>(smem + SM_RED);
-    float* red_m = reinterpret_cast<float*>(smem + SM_ML);
-    float* red_l = red_m + 4 * 16;
-    const int key_base = PREFIX ? 0 : p.prefix_len;  // position of local key 0
-    int it = 0;
-    bool ok = true, waited = false;
-    while (next_piece<PREFIX>(p, wk, x)) {
-        // this thread's two rows
-        uint32_t qf[4][4];
-        int vis[2];          // keys the row sees
-        bool rep[2];
-        const float *pa[2], *pr[2];  // a at local key j: pa[j]; r: pr[-j]
-        int vmin = INT_MAX;
+    float* red = reinterpret_cast<float*>(smem + L::RED);
+    float* red_m = reinterpret_cast<float*>(smem + L::ML);
+    float* red_l = red_m + NCW * ROWS;
+    float* mine = red + warp * ROWS * RED_PITCH;
+    const int lb = min(p.log_page, 6);
+    const int r0 = (lane & 3) * 2;  // this thread's rows of a block: r0, r0 + 1; its keys of a 16-key step: lane / 4, + 8
+    int it = 0;                     // tiles of the CTA before this item
+    uint32_t joins = 0;
+    bool ok = true, waited = false;  // a wait that gave up: no more waits, and the warp leaves at its next item
+    // A barrier of the consumer warps, bounded like every wait.
+    auto join_warps = [&] {
+        mbar_arrive_warp(bar_join);
+        if (ok) {
+            ok = mbar_wait_warp(bar_join, joins & 1, kWaitLimit);
+            if (!ok && lane == 0) report(p.err, 0x405);
+        }
+        ++joins;
+    };
+    for (int ni = 0;; ++ni) {
+        if (ok) {
+            ok = mbar_wait_warp(bar_item + 8 * (ni % NI), (ni / NI) & 1, kWaitLimit);
+            if (!ok && lane == 0) report(p.err, 0x404);
+        }
+        const Piece x = *reinterpret_cast<const Piece*>(smem + L::ITEM + 48 * (ni % NI));
+        const RowInfo* info = reinterpret_cast<const RowInfo*>(smem + L::INFO) + (ni % NI) * ROWS;
+        if (x.t1 < 0 || !ok) break;
+        uint32_t qf[NB][4][2];  // Q^T fragments; a replaced row's queries are not used
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const Row row = row_of<PREFIX>(p, x.b, x.g, x.rb * RT + wr * 16 + (lane >> 2) + 8 * u);
-            rep[u] = row.valid && p.replaced.get(row.h);
-            vis[u] = row.valid ? max(0, min(x.len, row.pos - key_base + 1)) : 0;
-            if (row.valid) vmin = min(vmin, vis[u]);
-            const size_t ph = (size_t)row.h * p.pattern_len;
-            pa[u] = p.a + ph + key_base;
-            pr[u] = p.r + ph + (row.pos - key_base);
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                p.q + (((size_t)row.b * p.H + row.h) * p.T + row.t) * kHeadDim + (lane & 3) * 2);
-            const bool read = row.valid && !rep[u];
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = nb * 8 + (lane >> 2);
+            const bool read = row < x.rows && !((x.replaced >> row) & 1u);
+            const uint32_t src = sbase + L::Q + ((ni % NI) * ROWS + row) * Q_PITCH + (lane & 3) * 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                qf[k][u] = read ? __ldg(src + 8 * k) : 0u;
-                qf[k][u + 2] = read ? __ldg(src + 8 * k + 4) : 0u;
+                qf[nb][k][0] = read ? ld_shared_u32(src + 32 * k) : 0u;
+                qf[nb][k][1] = read ? ld_shared_u32(src + 32 * k + 16) : 0u;
             }
         }
-        vmin = __reduce_min_sync(~0u, vmin);
-        const bool any_rep = __any_sync(~0u, rep[0] || rep[1]);
-        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f}, o[8][4];
+        // Running maximum (in units of the row's scores: dot products for an ordinary row), its log2(e) per unit, the sum
+        // (of this thread's keys) and O^T (columns 16 db + lane / 4, + 8), for this thread's two rows of each block.
+        float m[NB][2], o[4][NB][4];
+        uint64_t unit2[NB], l2[NB];
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
+        for (int nb = 0; nb < NB; ++nb) {
+            float un[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                m[nb][e] = kNegInf;
+                un[e] = ((x.replaced >> (nb * 8 + r0 + e)) & 1u) ? kLog2e : 0.125f * kLog2e;
+            }
+            unit2[nb] = f32x2(un[0], un[1]);
+            l2[nb] = 0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][nb][e] = 0.f;
+        }
+        // The warps' turns: a tile with K and V goes to one warp, one of V alone to two.
+        const int turns = x.keyed ? NCW : NCW / 2, turn = x.keyed ? warp : warp >> 1, sub = x.keyed ? 0 : warp & 1;
+        const int tk = x.keyed ? TK : 2 * TK;
+        int t = x.t0 + ((turn - it) & (turns - 1));
+        // A replaced row's scores of 64 keys are summed lane by lane (two each) into the warp's part of `red`, and
+        // read back in the fragment's order.  The first such row's are loaded a step ahead; the others of the same
+        // head then find theirs in L1.
+        float ahead[4];
+        auto load_ahead = [&](int key) {
+            const RowInfo& w = info[__ffs(x.replaced) - 1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = min(key + lane + 32 * e, w.vis - 1);
+                ahead[e] = __ldg(p.a + w.a0 + j);
+                ahead[2 + e] = __ldg(p.r + w.r0 - j);
+            }
+        };
+        if (x.replaced) load_ahead(t * tk + sub * TK);
 
-        for (int t = x.t0; t < x.t1; ++t, ++it) {
-            const int s = it % NS;
-            const int j0 = t * TK + wkey * KW + (lane & 3) * 2;  // this thread's keys: j0 + 8 nt + {0, 1}
-            float sc[NT][4];
-            if (any_rep) {  // read while the tile is on its way
+        for (; t < x.t1; t += turns) {
+            const unsigned at = (unsigned)(it + t - x.t0), s = at % NS;
+            const int k0 = t * tk + sub * TK;
+            const uint32_t sk = sbase + s * STAGE, sv = sk + (x.keyed || sub ? HALF : 0);
+            if (x.replaced) {
+                const int first = __ffs(x.replaced) - 1;
+                mine[first * RED_PITCH + lane] = ahead[0] + ahead[2];
+                mine[first * RED_PITCH + lane + 32] = ahead[1] + ahead[3];
+                load_ahead(k0 + turns * tk);
+                for (uint32_t left = x.replaced & (x.replaced - 1); left; left &= left - 1) {
+                    const int row = __ffs(left) - 1;
+                    const RowInfo& w = info[row];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int u = e >> 1, j = j0 + 8 * nt + (e & 1);
-                        sc[nt][e] = rep[u] && j < vis[u] ? __ldg(pa[u] + j) + __ldg(pr[u] - j) : 0.f;
-                    }
-            }
-            if (ok) {
-                ok = mbar_wait_warp(bar_full + 8 * s, (it / NS) & 1, kWaitLimit);
-                if (!ok && lane == 0) report(p.err, 0x402);
-            }
-            const uint32_t bad = meta[s];
-            const uint32_t sk = sbase + s * STAGE, sv = sk + HALF;
-            if (x.w == 2) {
-                float dot[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dot[nt][e] = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt += 2)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b[4];
-                        load_b_frag_nk(b, sk, wkey * KW + nt * 8, k * 16, lane);
-                        mma_bf16(dot[nt], qf[k], b[0], b[1]);
-                        mma_bf16(dot[nt + 1], qf[k], b[2], b[3]);
-                    }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!any_rep || !rep[e >> 1]) sc[nt][e] = dot[nt][e] * 0.125f;
-            }
-            // whole: every row of the warp sees every key of the tile
-            const bool whole = t * TK + TK <= vmin && bad == 0;
-            if (!whole) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + 8 * nt + (e & 1);
-                        if (j >= vis[e >> 1] || ((bad >> ((j & (TK - 1)) >> p.log_page)) & 1u)) sc[nt][e] = kNegInf;
-                    }
-            }
-            float f[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float mx = m[u];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mx = max3(mx, sc[nt][2 * u], sc[nt][2 * u + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                f[u] = mx > m[u] ? weight(m[u], mx) : 1.f;
-                m[u] = mx;
-                l[u] *= f[u];
-                const float base = mx == kNegInf ? 0.f : mx;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[nt][2 * u] = ex2((sc[nt][2 * u] - base) * kLog2e);
-                    sc[nt][2 * u + 1] = ex2((sc[nt][2 * u + 1] - base) * kLog2e);
-                    l[u] += sc[nt][2 * u] + sc[nt][2 * u + 1];
-                }
-            }
-            if (__any_sync(~0u, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    o[d][0] *= f[0];
-                    o[d][1] *= f[0];
-                    o[d][2] *= f[1];
-                    o[d][3] *= f[1];
-                }
-            }
-            // O += P V, P as a hi + lo bf16 pair: the tensor pipe has the room, and the
-            // weights then carry 16 bits
-#pragma unroll
-            for (int kk = 0; kk < NT; kk += 2) {
-                uint32_t ph[4], pl[4];
-                mma::pack_bf16_split(sc[kk][0], sc[kk][1], ph[0], pl[0]);
-                mma::pack_bf16_split(sc[kk][2], sc[kk][3], ph[1], pl[1]);
-                mma::pack_bf16_split(sc[kk + 1][0], sc[kk + 1][1], ph[2], pl[2]);
-                mma::pack_bf16_split(sc[kk + 1][2], sc[kk + 1][3], ph[3], pl[3]);
-                uint32_t keep[2] = {~0u, ~0u};
-                if (!whole) {  // a slot without a token may hold a NaN, and 0 times that is one
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int j = j0 + 8 * (kk + u);
-                        const bool dead = (bad >> ((j & (TK - 1)) >> p.log_page)) & 1u;
-                        keep[u] = dead ? 0u : (j < x.len ? 0xffffu : 0u) | (j + 1 < x.len ? 0xffff0000u : 0u);
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = min(k0 + lane + 32 * e, w.vis - 1);
+                        mine[row * RED_PITCH + lane + 32 * e] = __ldg(p.a + w.a0 + j) + __ldg(p.r + w.r0 - j);
                     }
                 }
+                __syncwarp();
+            }
+            // The stages are handed round, so a warp meets a stage's fills now and then.  Once the producer has issued this
+            // tile, the stage's fill before has been used up, and its barrier's parity can only tell of this one.
+            if (ok && *issued <= (int)at) {
+                const long long began = clock64();
+                while (*issued <= (int)at && ok) ok = clock64() - began < kWaitLimit;
+            }
+            ok = __all_sync(~0u, ok);
+            if (ok) ok = mbar_wait_warp(bar_full + 8 * s, (at / NS) & 1, kWaitLimit);
+            if (!ok && lane == 0) report(p.err, 0x402);
+            const uint32_t bad = meta[s] >> (sub ? TK >> lb : 0);
+            const bool whole = k0 + TK <= x.vmin && bad == 0;  // every row sees every key
 #pragma unroll
-                for (int d = 0; d < 8; d += 2) {
-                    uint32_t b[4];
-                    load_b_frag_kn(b, sv, d * 8, wkey * KW + kk * 8, lane);
-                    if (!whole) {
-                        b[0] &= keep[0];
-                        b[1] &= keep[1];
-                        b[2] &= keep[0];
-                        b[3] &= keep[1];
+            for (int kc = 0; kc < TK; kc += L::KC) {
+                float st[KB][NB][4];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) st[kb][nb][e] = 0.f;
+                if (x.keyed) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) {
+                            uint32_t a[4];
+                            mma::load_a_frag(a, sk, kc + kb * 16, k * 16, lane);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) mma_bf16(st[kb][nb], a, qf[nb][k][0], qf[nb][k][1]);
+                        }
+                }
+                if (x.replaced) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if ((x.replaced >> (nb * 8 + r0 + e)) & 1u) {
+                                const float* src = mine + (nb * 8 + r0 + e) * RED_PITCH + kc + (lane >> 2);
+#pragma unroll
+                                for (int kb = 0; kb < KB; ++kb) {
+                                    st[kb][nb][e] = src[kb * 16];
+                                    st[kb][nb][2 + e] = src[kb * 16 + 8];
+                                }
+                            }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const int v0 = info[nb * 8 + r0].vis, v1 = info[nb * 8 + r0 + 1].vis;
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int jl = kc + kb * 16 + (lane >> 2) + 8 * (e >> 1);
+                                if (k0 + jl >= ((e & 1) ? v1 : v0) || ((bad >> (jl >> lb)) & 1u)) st[kb][nb][e] = kNegInf;
+                            }
                     }
-                    mma_bf16(o[d], ph, b[0], b[1]);
-                    mma_bf16(o[d + 1], ph, b[2], b[3]);
-                    mma_bf16(o[d], pl, b[0], b[1]);
-                    mma_bf16(o[d + 1], pl, b[2], b[3]);
+                }
+                // The maximum moves only when a score passes it by more than 2^8: P and the sums stay far from fp32's limits,
+                // and most steps need no reduction across the lanes and no rescaling.
+                bool grow = false;
+                float mx[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const float2 un = split_f32x2(unit2[nb]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = fmaxf(st[0][nb][e], st[0][nb][2 + e]);
+#pragma unroll
+                        for (int kb = 1; kb < KB; ++kb) v = max3(v, st[kb][nb][e], st[kb][nb][2 + e]);
+                        mx[nb][e] = v;
+                        grow |= (v - m[nb][e]) * (e ? un.y : un.x) > 8.f;
+                    }
+                }
+                if (__any_sync(~0u, grow)) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const float2 un = split_f32x2(unit2[nb]);
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = mx[nb][e];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, d));
+                            const float u = e ? un.y : un.x;
+                            const bool up = (v - m[nb][e]) * u > 8.f;
+                            f[e] = up ? ex2((m[nb][e] - v) * u) : 1.f;
+                            if (up) m[nb][e] = v;
+                        }
+                        l2[nb] = mul_f32x2(l2[nb], f32x2(f[0], f[1]));
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[d][nb][e] *= f[e & 1];
+                    }
+                }
+                // P^T, rounded, turned into the second product's B fragments
+                uint32_t ph[KB][NB][2], pl[KB][NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    // (x - m) * unit, not x * unit - m * unit: the products may overflow where the difference is small
+                    const uint64_t base2 = f32x2(m[nb][0] == kNegInf ? 0.f : m[nb][0], m[nb][1] == kNegInf ? 0.f : m[nb][1]);
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float2 e =
+                                split_f32x2(mul_f32x2(sub_f32x2(f32x2(st[kb][nb][2 * u], st[kb][nb][2 * u + 1]), base2), unit2[nb]));
+                            const float p0 = ex2(e.x), p1 = ex2(e.y);
+                            l2[nb] = add_f32x2(l2[nb], f32x2(p0, p1));
+                            if (SPLIT_P) {
+                                uint32_t hi, lo;
+                                mma::pack_bf16_split(p0, p1, hi, lo);
+                                ph[kb][nb][u] = transpose8(hi);
+                                pl[kb][nb][u] = transpose8(lo);
+                            } else {
+                                ph[kb][nb][u] = transpose8(pack_bf16x2(p0, p1));
+                            }
+                        }
+                }
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    uint32_t keep[2] = {~0u, ~0u};
+                    if (!whole) {  // a slot without a token may hold a NaN, and 0 times that is one
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int jl = kc + kb * 16 + 8 * u + r0, j = k0 + jl;
+                            const bool dead = (bad >> (jl >> lb)) & 1u;
+                            keep[u] = dead ? 0u : (j < x.len ? 0xffffu : 0u) | (j + 1 < x.len ? 0xffff0000u : 0u);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        // V^T: 16 columns x 16 keys, from V stored [key][column]
+                        uint32_t a[4];
+                        const int key = kc + kb * 16 + (lane & 7) + (lane >> 4) * 8, col = d * 16 + ((lane >> 3) & 1) * 8;
+                        mma::ldsm_x4_t(a[0], a[1], a[2], a[3], sv + mma::swz(key, col));
+                        if (!whole) {
+                            a[0] &= keep[0];
+                            a[1] &= keep[0];
+                            a[2] &= keep[1];
+                            a[3] &= keep[1];
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma_bf16(o[d][nb], a, ph[kb][nb][0], ph[kb][nb][1]);
+                            if (SPLIT_P) mma_bf16(o[d][nb], a, pl[kb][nb][0], pl[kb][nb][1]);
+                        }
+                    }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+            if (lane == 0) mbar_arrive_n(bar_empty + 8 * s, x.keyed ? 2 : 1);
         }
+        it += x.t1 - x.t0;
 
         // ---- the warps' parts to shared memory, joined over the keys
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            l[u] += __shfl_xor_sync(~0u, l[u], 1);
-            l[u] += __shfl_xor_sync(~0u, l[u], 2);
-            const int row = (lane >> 2) + 8 * u;
-            if ((lane & 3) == 0) {
-                red_m[warp * 16 + row] = m[u];
-                red_l[warp * 16 + row] = l[u];
-            }
+        for (int nb = 0; nb < NB; ++nb) {
+            const float2 ll = split_f32x2(l2[nb]);
 #pragma unroll
-            for (int d = 0; d < 8; ++d)
-                *reinterpret_cast<float2*>(red + (warp * 16 + row) * RED_PITCH + d * 8 + (lane & 3) * 2) =
-                    make_float2(o[d][2 * u], o[d][2 * u + 1]);
+            for (int e = 0; e < 2; ++e) {
+                const int row = nb * 8 + r0 + e;
+                float l = e ? ll.y : ll.x;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
+                if (lane < 4) {
+                    red_m[warp * ROWS + row] = ((x.replaced >> row) & 1u) ? m[nb][e] : 0.125f * m[nb][e];
+                    red_l[warp * ROWS + row] = l;
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    mine[row * RED_PITCH + d * 16 + (lane >> 2)] = o[d][nb][e];
+                    mine[row * RED_PITCH + d * 16 + (lane >> 2) + 8] = o[d][nb][2 + e];
+                }
+            }
         }
-        named_sync(1, NCONS);
-        const int c_first = cta_of(x.start), pieces = cta_of(x.start + (long long)(x.n - 1) * x.w) - c_first + 1;
-        const int rows = min(RT, p.rows - x.rb * RT);
+        join_warps();
         const int c = (tid & 15) * 4;
         if (!PREFIX && p.part && !waited) {
             griddep_wait();
             waited = true;
         }
         float* slot = p.slots + ((size_t)blockIdx.x * 2 + (x.t0 == 0)) * SLOT;
-        for (int row = tid >> 4; row < rows; row += NCONS / 16) {
-            const int w0 = (row >> 4) * WK, rl = row & 15;
+        for (int row = tid >> 4; row < x.rows; row += NCONS / 16) {
             float mm = kNegInf;
 #pragma unroll
-            for (int k = 0; k < WK; ++k) mm = fmaxf(mm, red_m[(w0 + k) * 16 + rl]);
+            for (int k = 0; k < NCW; ++k) mm = fmaxf(mm, red_m[k * ROWS + row]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float ll = 0.f;
 #pragma unroll
-            for (int k = 0; k < WK; ++k) {
-                const float f = weight(red_m[(w0 + k) * 16 + rl], mm);
-                const float4 v = *reinterpret_cast<const float4*>(red + ((w0 + k) * 16 + rl) * RED_PITCH + c);
+            for (int k = 0; k < NCW; ++k) {
+                const float f = weight(red_m[k * ROWS + row], mm);
+                const float4 v = *reinterpret_cast<const float4*>(red + (k * ROWS + row) * RED_PITCH + c);
                 acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
-                ll += f * red_l[(w0 + k) * 16 + rl];
+                ll += f * red_l[k * ROWS + row];
             }
-            if (pieces == 1) {
-                finish_row<PREFIX>(p, x.b, x.g, x.rb * RT + row, c, acc, mm, ll);
+            if (x.pieces == 1) {
+                finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + c), acc);
                 if (c == 0) {
-                    __stcg(slot + RT * kHeadDim + row, mm);
-                    __stcg(slot + RT * (kHeadDim + 1) + row, ll);
+                    __stcg(slot + ROWS * kHeadDim + row, mm);
+                    __stcg(slot + ROWS * (kHeadDim + 1) + row, ll);
                 }
             }
         }
-        if (pieces > 1) {
+        if (x.pieces > 1) {
             __threadfence();
-            named_sync(1, NCONS);
-            if (tid == 0) *last_flag = atomicAdd(p.counters + c_first, 1u) == (unsigned)pieces - 1;
-            named_sync(1, NCONS);
-            if (*last_flag) {
+            join_warps();
+            if (tid == 0) *last_flag = atomicAdd(p.counters + x.c_first, 1u) == (unsigned)x.pieces - 1;
+            join_warps();
+            if (*last_flag && ok) {
                 __threadfence();
-                auto slot_of = [&](int k) { return p.slots + ((size_t)(c_first + k) * 2 + (k == 0)) * SLOT; };
-                for (int row = tid >> 4; row < rows; row += NCONS / 16) {
+                auto slot_of = [&](int k) { return p.slots + ((size_t)(x.c_first + k) * 2 + (k == 0)) * SLOT; };
+                for (int row = tid >> 4; row < x.rows; row += NCONS / 16) {
                     float mm = kNegInf;
-                    for (int k = tid & 15; k < pieces; k += 16) mm = fmaxf(mm, __ldcg(slot_of(k) + RT * kHeadDim + row));
+                    for (int k = tid & 15; k < x.pieces; k += 16) mm = fmaxf(mm, __ldcg(slot_of(k) + ROWS * kHeadDim + row));
                     // the sixteen threads of a row are a half-warp that runs this loop together
                     const uint32_t half = 0xffffu << (lane & 16);
 #pragma unroll
@@ -543,19 +757,20 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float ll = 0.f;
 #pragma unroll 4
-                    for (int k = 0; k < pieces; ++k) {
+                    for (int k = 0; k < x.pieces; ++k) {
                         const float* sl = slot_of(k);
-                        const float f = weight(__ldcg(sl + RT * kHeadDim + row), mm);
+                        const float f = weight(__ldcg(sl + ROWS * kHeadDim + row), mm);
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + row * kHeadDim + c));
                         acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
-                        ll += f * __ldcg(sl + RT * (kHeadDim + 1) + row);
+                        ll += f * __ldcg(sl + ROWS * (kHeadDim + 1) + row);
                     }
-                    finish_row<PREFIX>(p, x.b, x.g, x.rb * RT + row, c, acc, mm, ll);
+                    finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
                 }
-                if (tid == 0) atomicExch(p.counters + c_first, 0u);
+                if (tid == 0) atomicExch(p.counters + x.c_first, 0u);
             }
         }
-        named_sync(1, NCONS);  // the shared parts have been read
+        join_warps();  // the shared parts have been read
+        if (lane == 0) mbar_arrive(bar_taken + 8 * (ni % NI));
     }
 }
 
@@ -595,7 +810,9 @@ bool make_tmap_pages(const saf_paged_kv& kv, bool keys, CUtensorMap* out) {
 struct PagedWs {
     size_t counters[2], slots[2], part, total;
 };
-int row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Rows are dealt in blocks of up to 32, as even as eight allows.
+int row_blocks(int rows) { return (rows + 8 * kMaxBlocks - 1) / (8 * kMaxBlocks); }
+int block_rows(int rows) { return ((rows + row_blocks(rows) - 1) / row_blocks(rows) + 7) & ~7; }
 PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
     PagedWs w{};
     const int R = H / H_kv * T;
@@ -606,8 +823,7 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
     }
     for (int k = 0; k < (prefix_len > 0 ? 2 : 1); ++k) {
         w.slots[k] = off;
-        const int rows = (int)std::min<int64_t>(64, k ? (int64_t)B * R : R);
-        off = align256(off + sizeof(float) * 2 * kMaxGrid * 16 * row_warps(rows) * (kHeadDim + 2));
+        off = align256(off + sizeof(float) * 2 * kMaxGrid * block_rows(k ? B * R : R) * (kHeadDim + 2));
     }
     w.part = off;
     if (prefix_len > 0) off = align256(off + sizeof(float) * (size_t)B * H * T * (kHeadDim + 2));
@@ -615,16 +831,16 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
     return w;
 }
 
-template <int WR, bool PREFIX>
+template <int NB, bool PREFIX>
 cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const SplitParams& p, bool overlap,
                          cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<WR, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)SM_ALLOC);
+    cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NB, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Smem<NB>::TOTAL);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min(kMaxGrid, CTAS_PER_SM * sm_count()));
-    cfg.blockDim = dim3(NCONS + 32);
-    cfg.dynamicSmemBytes = SM_ALLOC;
+    cfg.blockDim = dim3(32 * (Smem<NB>::NCW + 1));
+    cfg.dynamicSmemBytes = Smem<NB>::TOTAL;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -633,7 +849,7 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Spl
     cfg.numAttrs = overlap ? 1 : 0;
     const int kid = PREFIX ? KID_PAGED_PREFIX : KID_PAGED_ATTN;
     launch_begin(kid, stream);
-    e = cudaLaunchKernelEx(&cfg, paged_split_kernel<WR, PREFIX>, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, paged_split_kernel<NB, PREFIX>, mk, mv, p);
     launch_end(kid, stream);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -642,14 +858,18 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Spl
 template <bool PREFIX>
 cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, SplitParams& p, bool overlap,
                               cudaStream_t stream) {
-    const int wr = row_warps(p.rows);
-    p.nrb = (p.rows + 16 * wr - 1) / (16 * wr);
-    // the tile axis in the kernel's integers: a sequence's units and all tiles in 31 bits
-    const double most = std::max(1, (std::max(p.max_len, p.prefix_len) + TK - 1) / TK);
-    if (most * p.nrb * p.wsum >= 2147483648.0 || most * p.nseq >= 2147483648.0) return cudaErrorNotSupported;
-    switch (wr) {
+    const int per = block_rows(p.rows);
+    p.nrb = (p.rows + per - 1) / per;
+    p.by_T = divisor(p.T);
+    p.by_R = divisor(p.R);
+    p.by_nrb = divisor(p.nrb);
+    // all units in 31 bits
+    const double most = kItem + std::max(1, (std::max(p.max_len, p.prefix_len) + TK - 1) / TK);
+    if (most * p.nrb * p.Hkv * p.nseq >= 2147483648.0) return cudaErrorNotSupported;
+    switch (per / 8) {
         case 1: return launch_split<1, PREFIX>(mk, mv, p, overlap, stream);
         case 2: return launch_split<2, PREFIX>(mk, mv, p, overlap, stream);
+        case 3: return launch_split<3, PREFIX>(mk, mv, p, overlap, stream);
         default: return launch_split<4, PREFIX>(mk, mv, p, overlap, stream);
     }
 }
@@ -673,7 +893,6 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.pattern_len = c.pattern_len;
     p.prefix_len = c.prefix_len;
     p.replaced = c.replaced;
-    p.keyless = c.keyless;
     p.seq_lens = c.seq_lens;
     p.q_lens = c.q_lens;
     p.num_pages = c.kv.num_pages;
@@ -685,8 +904,12 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.G = c.H / c.kv.H_kv;
     p.R = p.G * c.T;
     p.max_len = c.max_len;
-    for (int g = 0; g < p.Hkv; ++g)
-        for (int k = c.keyless.get(g) ? 1 : 2; k > 0; --k) p.g_of_w[p.wsum++] = (uint8_t)g;
+    int n = 0;
+    for (int want = 0; want < 2; ++want) {  // those with keys, then those without
+        for (int g = 0; g < p.Hkv; ++g)
+            if (c.keyless.get(g) == (want == 1)) p.order[n++] = (uint8_t)g;
+        if (want == 0) p.keyed = n;
+    }
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
         p.part = reinterpret_cast<float*>(c.ws + w.part);
