@@ -32,10 +32,6 @@
 // One new token makes this a stream of K and V at a few flops per byte: HBM
 // bounds it, so the warp-level MMAs are enough, and the kernel is built for bytes
 // in flight and short chains.
-#include <limits.h>
-
-#include <algorithm>
-
 #include "mma_util.cuh"
 #include "saf_paged.cuh"
 
@@ -63,15 +59,6 @@ struct Piece {
     int len, keyed, t0, t1, pieces, c_first, rows, vmin;
     uint32_t replaced;
 };
-// One row of an item.  A replaced row looks its scores up: a at local key j is
-// a[a0 + j], r is r[r0 - j], for j < vis.
-struct RowInfo {
-    long long a0, r0;
-    int vis;        // keys it sees
-    int out, part;  // its row of the output (-1: it has no token), and of the prefix's parts
-    int replaced;
-};
-
 // Shared memory of a CTA whose items hold up to 8 NB rows, two CTAs to an SM.
 template <int NB>
 struct Smem {
@@ -91,52 +78,6 @@ struct Smem {
 };
 static_assert(sizeof(Piece) <= 48 && sizeof(RowInfo) == 32, "shared memory slots");
 
-// Division by a launch constant: n / d = (umulhi(n, m) + n) >> s for 0 <= n < 2^31, with 2^(s-1) < d <= 2^s and
-// m = floor(2^32 (2^s - d) / d) + 1 (the round-up method of Granlund and Montgomery).  A few cycles, where the
-// general division's code, cold at the start of a launch, costs hundreds.
-struct Divisor {
-    uint32_t m, s;
-    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
-};
-inline Divisor divisor(int d) {
-    Divisor x{0, 0};
-    while ((1ll << x.s) < d) ++x.s;
-    x.m = (uint32_t)(((1ull << 32) * ((1ull << x.s) - (uint64_t)d)) / (uint64_t)d + 1);
-    return x;
-}
-
-struct SplitParams {
-    const __nv_bfloat16* q;
-    __nv_bfloat16* o;
-    float* lse;
-    const float *a, *r;
-    int pattern_len, prefix_len;
-    HeadBits replaced;
-    const int32_t *table, *seq_lens, *q_lens;
-    int table_stride, num_pages, log_page, Hkv;
-    int B, H, T, G, R, max_len;  // R = G T rows of one (b, g)
-    int nseq, rows, nrb;         // key sequences, rows of one item list entry, row blocks
-    Divisor by_T, by_R, by_nrb;
-    int keyed;                   // K/V heads with keys: the first of order[]
-    uint8_t order[kMaxHeads];    // K/V heads, those with keys first
-    unsigned int *err, *counters;
-    float* slots;                // pieces: two per CTA
-    float* part;                 // [Hkv * B * R][64] O, then [Hkv * B * R] m, then l, of the prefix (or null)
-};
-
-__device__ __forceinline__ void report(unsigned int* err, unsigned int code) {
-    atomicOr(err, 1u);
-    atomicCAS(err + 1, 0u, code);
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                            int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];\n" ::
-            "r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-        : "memory");
-}
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n) : "memory");
 }
@@ -147,23 +88,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// exp(x - m) for finite or -inf x <= m (m = -inf: no weight yet).
-__device__ __forceinline__ float weight(float x, float m) { return ex2((x - (m == kNegInf ? 0.f : m)) * kLog2e); }
-
-template <bool PREFIX>
-__device__ __forceinline__ int key_len(const SplitParams& p, int b) {
-    return PREFIX ? p.prefix_len : min(max(p.seq_lens[b], 0), p.max_len);
-}
-__device__ __forceinline__ int new_tokens(const SplitParams& p, int b) {
-    return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
-}
 // Tiles of an item (one without keys still takes one, empty, tile: its rows are written).
 __device__ __forceinline__ int tiles_of(int len, bool keyed) {
     const int tk = keyed ? TK : 2 * TK;
     return max(1, (len + tk - 1) / tk);
 }
 // Units of a sequence on the axis.
-__device__ __forceinline__ int seq_units(const SplitParams& p, int len) {
+__device__ __forceinline__ int seq_units(const PagedParams& p, int len) {
     return p.nrb * (p.keyed * (tiles_of(len, true) + kItem) + (p.Hkv - p.keyed) * (tiles_of(len, false) + kItem));
 }
 
@@ -172,7 +103,7 @@ struct Item {
     int gi, rb, n, start;  // its tiles, its first unit
     bool keyed;
 };
-__device__ __forceinline__ Item item_at(const SplitParams& p, int base, int len, int u) {
+__device__ __forceinline__ Item item_at(const PagedParams& p, int base, int len, int u) {
     Item x;
     int off = u - base;
     x.n = tiles_of(len, true);
@@ -192,69 +123,10 @@ __device__ __forceinline__ Item item_at(const SplitParams& p, int base, int len,
     return x;
 }
 
-// Row rr of the item list entry (b, g); n, pos0: the sequence's new tokens and
-// the position of the first (with PREFIX they are looked up per row).
-template <bool PREFIX>
-__device__ __forceinline__ RowInfo row_info(const SplitParams& p, int b, int g, int len, int n, int pos0, int rr) {
-    RowInfo x;
-    x.a0 = x.r0 = 0;
-    x.vis = x.part = 0;
-    x.out = -1;
-    x.replaced = 0;
-    if (rr >= p.rows) return x;
-    const int rb = PREFIX ? p.by_R.div(rr) : b, rem = PREFIX ? rr - rb * p.R : rr;
-    const int u = p.by_T.div(rem), h = g * p.G + u, t = rem - u * p.T;
-    if (PREFIX) {
-        n = new_tokens(p, rb);
-        pos0 = p.prefix_len + key_len<false>(p, rb) - n;
-    }
-    if (t >= n) return x;
-    const int key_base = PREFIX ? 0 : p.prefix_len;  // position of local key 0
-    const long long ph = (long long)h * p.pattern_len;
-    x.vis = max(0, min(len, pos0 + t - key_base + 1));
-    x.a0 = ph + key_base;
-    x.r0 = ph + pos0 + t - key_base;
-    x.out = (rb * p.H + h) * p.T + t;
-    x.part = (g * p.B + rb) * p.R + rem;
-    x.replaced = p.replaced.get(h);
-    return x;
-}
-
-// A finished row (four columns from c): with PREFIX the part that the batch's
-// own keys are joined to, else the output, after joining the prefix's part.
-template <bool PREFIX>
-__device__ __forceinline__ void finish_row(const SplitParams& p, const RowInfo& x, int c, float4 o, float m, float l) {
-    if (x.out < 0) return;
-    const size_t nrow = (size_t)p.Hkv * p.B * p.R;
-    float* part = p.part + (size_t)x.part * kHeadDim + c;
-    float* part_m = p.part + nrow * kHeadDim + x.part;
-    if (PREFIX) {
-        *reinterpret_cast<float4*>(part) = o;
-        if (c == 0) {
-            part_m[0] = m;
-            part_m[nrow] = l;
-        }
-        return;
-    }
-    if (p.part) {
-        const float4 o2 = __ldcg(reinterpret_cast<const float4*>(part));
-        const float m2 = __ldcg(part_m), l2 = __ldcg(part_m + nrow);
-        const float mm = fmaxf(m, m2), f = weight(m, mm), f2 = weight(m2, mm);
-        o = make_float4(o.x * f + o2.x * f2, o.y * f + o2.y * f2, o.z * f + o2.z * f2, o.w * f + o2.w * f2);
-        l = l * f + l2 * f2;
-        m = mm;
-    }
-    const bool some = !(l == 0.f);  // also a NaN
-    const float s = some ? __fdividef(1.f, l) : 0.f;
-    *reinterpret_cast<uint2*>(p.o + (size_t)x.out * kHeadDim + c) =
-        make_uint2(pack_bf16x2(o.x * s, o.y * s), pack_bf16x2(o.z * s, o.w * s));
-    if (c == 0) p.lse[x.out] = some ? m + __logf(l) : kNegInf;
-}
-
 template <int NB, bool PREFIX>
 __global__ void __launch_bounds__(32 * (Smem<NB>::NCW + 1), CTAS_PER_SM)
 paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                   const __grid_constant__ SplitParams p) {
+                   const __grid_constant__ PagedParams p) {
     using L = Smem<NB>;
     constexpr int ROWS = L::ROWS, NCW = L::NCW, NS = L::NS, NI = L::NI, KB = L::KC / 16, NCONS = 32 * NCW;
     // P as one bf16 (half a step of 2^-8 off, as in the layer's own forward), or as a hi + lo pair of 16 bits where
@@ -453,6 +325,17 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             if (!ok && lane == 0) report(p.err, 0x405);
         }
         ++joins;
+    };
+    // A finished row (four columns from c): with PREFIX the part that the batch's own keys are joined to.
+    auto finish = [&](const RowInfo& row, int c, float4 acc, float mm, float ll) {
+        if (row.out < 0) return;
+        if (PREFIX) {
+            *reinterpret_cast<float4*>(part_o(p, 0, row.part) + c) = acc;
+            if (c == 0) store_part_ml(p, 0, row.part, mm, ll);
+        } else {
+            if (p.part) join_parts(p, row.part, c, acc, mm, ll);
+            store_row(p, row, c, acc, mm, ll);
+        }
     };
     for (int ni = 0;; ++ni) {
         if (ok) {
@@ -730,7 +613,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 ll += f * red_l[k * ROWS + row];
             }
             if (x.pieces == 1) {
-                finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
+                finish(info[row], c, acc, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + c), acc);
                 if (c == 0) {
@@ -764,7 +647,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
                         ll += f * __ldcg(sl + ROWS * (kHeadDim + 1) + row);
                     }
-                    finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
+                    finish(info[row], c, acc, mm, ll);
                 }
                 if (tid == 0) atomicExch(p.counters + x.c_first, 0u);
             }
@@ -775,44 +658,19 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    return fn;
-}
-
-// The cache as (d, slot, head, page), boxes of one page's rows (64 at most).
-bool make_tmap_pages(const saf_paged_kv& kv, bool keys, CUtensorMap* out) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const int64_t st[3] = {keys ? kv.k_stride_slot : kv.v_stride_slot, keys ? kv.k_stride_head : kv.v_stride_head,
-                           keys ? kv.k_stride_page : kv.v_stride_page};
-    cuuint64_t dims[4] = {64, (cuuint64_t)kv.page_size, (cuuint64_t)kv.H_kv, (cuuint64_t)std::max(1, kv.num_pages)};
-    cuuint64_t strides[3] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)std::min(TK, kv.page_size), 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, keys ? kv.k : kv.v, dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Workspace: header, the two launches' piece counters, their pieces, the prefix's parts.
-struct PagedWs {
-    size_t counters[2], slots[2], part, total;
-};
 // Rows are dealt in blocks of up to 32, as even as eight allows.
 int row_blocks(int rows) { return (rows + 8 * kMaxBlocks - 1) / (8 * kMaxBlocks); }
 int block_rows(int rows) { return ((rows + row_blocks(rows) - 1) / row_blocks(rows) + 7) & ~7; }
+
+// Items of more rows than this go to the tensor-core kernel.
+constexpr int kTcRows = 32;
+
+// Workspace: header, the two launches' piece counters, the pieces of the one
+// that joins them, the prefix's parts.  Sizes bound every choice of kernel and
+// split, so that they grow with each argument.
+struct PagedWs {
+    size_t counters[2], slots[2], part, total;
+};
 PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
     PagedWs w{};
     const int R = H / H_kv * T;
@@ -821,18 +679,23 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
         w.counters[k] = off;
         off += kMaxGrid * sizeof(unsigned int);
     }
+    auto split_slots = [](int64_t rows) { return 2 * kMaxGrid * std::min<int64_t>(8 * kMaxBlocks, (rows + 7) & ~7ll); };
+    auto tc_rows = [](int64_t items) { return 128 * (kTcCtas + items); };  // items * splits <= kTcCtas + items
     for (int k = 0; k < (prefix_len > 0 ? 2 : 1); ++k) {
         w.slots[k] = off;
-        off = align256(off + sizeof(float) * 2 * kMaxGrid * block_rows(k ? B * R : R) * (kHeadDim + 2));
+        const int64_t rows = k ? (int64_t)B * R : R;
+        int64_t need = split_slots(rows);
+        if (k == 0 && rows > kTcRows) need = std::max<int64_t>(need, tc_rows(std::min(kTcCtas, tc_items(B, H_kv, R))));
+        off = align256(off + sizeof(float) * (size_t)need * (kHeadDim + 2));
     }
     w.part = off;
-    if (prefix_len > 0) off = align256(off + sizeof(float) * (size_t)B * H * T * (kHeadDim + 2));
+    if (prefix_len > 0) off = align256(off + sizeof(float) * (size_t)tc_rows(tc_items(1, H_kv, B * R)) * (kHeadDim + 2));
     w.total = off;
     return w;
 }
 
 template <int NB, bool PREFIX>
-cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const SplitParams& p, bool overlap,
+cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const PagedParams& p, bool overlap,
                          cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NB, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem<NB>::TOTAL);
@@ -856,7 +719,7 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Spl
 }
 
 template <bool PREFIX>
-cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, SplitParams& p, bool overlap,
+cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, bool overlap,
                               cudaStream_t stream) {
     const int per = block_rows(p.rows);
     p.nrb = (p.rows + per - 1) / per;
@@ -882,9 +745,9 @@ size_t paged_workspace_bytes(int B, int H, int H_kv, int T, int prefix_len) {
 
 cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     CUtensorMap mk, mv;
-    if (!make_tmap_pages(c.kv, true, &mk) || !make_tmap_pages(c.kv, false, &mv)) return cudaErrorNotSupported;
+    if (!make_tmap_pages(c.kv, true, TK, &mk) || !make_tmap_pages(c.kv, false, TK, &mv)) return cudaErrorNotSupported;
     const PagedWs w = paged_ws(c.B, c.H, c.kv.H_kv, c.T, c.prefix_len);
-    SplitParams p{};
+    PagedParams p{};
     p.q = c.q;
     p.o = c.o;
     p.lse = c.lse;
@@ -919,7 +782,11 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
         p.rows = c.B * p.R;
         p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[1]);
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
-        const cudaError_t e = launch_split_rows<true>(mk, mv, p, false, stream);
+        const bool tc = p.rows > kTcRows;
+        p.splits = tc ? tc_splits(tc_items(1, p.Hkv, p.rows), c.prefix_len) : 1;
+        p.parts = p.splits;
+        const cudaError_t e = tc ? launch_paged_tc(c.kv, p, true, false, stream)
+                                 : launch_split_rows<true>(mk, mv, p, false, stream);
         if (e != cudaSuccess) return e;
     }
     p.table = c.page_table;
@@ -928,7 +795,9 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.rows = p.R;
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
-    return launch_split_rows<false>(mk, mv, p, c.prefix_len > 0, stream);
+    if (p.rows <= kTcRows) return launch_split_rows<false>(mk, mv, p, c.prefix_len > 0, stream);
+    p.splits = tc_splits(tc_items(c.B, p.Hkv, p.rows), c.max_len);
+    return launch_paged_tc(c.kv, p, false, c.prefix_len > 0, stream);
 }
 
 }  // namespace saf

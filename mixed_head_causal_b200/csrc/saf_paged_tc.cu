@@ -1,0 +1,571 @@
+// Attention of many rows over the paged key/value cache on the 5th-generation
+// tensor cores: prompt chunks, and a shared prefix seen by a whole batch.
+//
+// A CTA takes 128 rows of one K/V head (its query heads times the new tokens, and
+// with a shared prefix times the sequences) and one stretch of their keys, in
+// blocks of 128.  Two CTAs per SM, six warps each:
+//   warp 0      producer: page look-up and TMA loads, a box per page, two stages each
+//               of K and V (no K for a K/V head whose query heads are all replaced)
+//   warp 1      TMEM owner and MMA issuer (one elected lane):
+//               S = Q K^T  (tcgen05 SS, 128x128x64), O += P V  (TS, 128x64x128)
+//   warps 2..5  one row per thread: its queries to shared memory, then per block the
+//               scores out of TMEM, the running maximum (moved only when a score
+//               passes it by 2^8), P = exp(s - m) as bf16 into TMEM (half a step of
+//               2^-8 off, as in the layer's forward), the sum in fp32
+// S_{j+1} is issued as soon as the rows have copied S_j to registers, before P V_j.
+//   ordinary row   s = q . k / 8
+//   replaced row   s = a[j] + r[i - j]: 32 keys at a time, a warp reads each of its
+//                  replaced rows' stretch of r side by side (lane = key) into shared
+//                  memory and every thread takes its own row from there
+// With a prefix each stretch is a part that the batch's own keys are joined to;
+// otherwise a row of one stretch is written at once, and of several by the CTA that
+// finishes the row block's last one, in key order.
+//
+// Per block and row: 128 exponentials against 2 x 128 x 64 multiply-adds, so the exp
+// unit (16 a cycle and SM: 2048 cycles for the two CTAs' blocks) bounds it before
+// the tensor pipe (about 770 cycles a block).
+#include "saf_paged.cuh"
+
+namespace saf {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128, BN = 128;  // rows per CTA, keys per block
+constexpr int NST = 2;             // K and V stages
+constexpr int NTHREADS = 192;
+constexpr uint32_t TILE_BYTES = 128 * 64 * 2;
+constexpr uint32_t TMEM_COLS = 256;
+constexpr uint32_t TO_COL = 128, TP_COL = 192;  // S in 0..127, O, P
+constexpr long long kWaitLimit = 1ll << 31;
+
+// shared memory map (offsets from a 1024-aligned base)
+constexpr uint32_t SM_Q = 0;
+constexpr uint32_t SM_K = SM_Q + TILE_BYTES;
+constexpr uint32_t SM_V = SM_K + NST * TILE_BYTES;
+constexpr int PAT_PITCH = 33;                               // floats: a warp's reads of its 32 rows hit distinct banks
+constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;        // [4 warps][32 rows][PAT_PITCH]
+constexpr uint32_t SM_ROW = SM_PAT + 4 * 32 * PAT_PITCH * 4;  // [128] {a0, r0} of a row
+constexpr uint32_t SM_BAR = SM_ROW + 128 * 16;
+constexpr uint32_t SM_MISC = SM_BAR + 16 * 8;  // TMEM address, last flag, [2] boxes without a page, [4] largest vis of a row warp
+constexpr uint32_t SM_TOTAL = SM_MISC + 64;
+
+// Row max of 128 raw scores: three-input max, four independent chains.
+__device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
+    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+    for (int e = 0; e < 128; e += 2)
+        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// P = exp2(s * unit - m * unit) of keys [32 Q, 32 Q + 32) as 16 bf16 pairs, their sum added to l2.
+template <int Q>
+__device__ __forceinline__ void exp_quarter(const uint32_t (&v)[128], uint64_t unit2, uint64_t nm2, uint64_t (&l2)[4],
+                                            uint32_t tP) {
+    uint32_t pw[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 x =
+            split_f32x2(fma_f32x2(f32x2(__uint_as_float(v[32 * Q + e]), __uint_as_float(v[32 * Q + e + 1])), unit2, nm2));
+        const float p0 = ex2(x.x), p1 = ex2(x.y);
+        l2[(e >> 1) & 3] = add_f32x2(l2[(e >> 1) & 3], f32x2(p0, p1));
+        pw[e >> 1] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(tP + 16 * Q, pw);
+}
+
+// This warp's 32 O rows times f.
+__device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(tO + 32 * c, ov);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+        tmem_st32(tO + 32 * c, ov);
+    }
+}
+
+// What a row thread keeps between blocks, and what it looks scores up by.
+struct RowState {
+    float m, l;  // running maximum (in units of the row's scores), sum
+    float unit;  // log2(e) per unit: dot products are 8 of a score
+    int vis;
+};
+struct Patterns {
+    const float *a, *r;
+    const longlong2* rows;  // {a0, r0} of the warp's rows
+    float* pat;             // the warp's staging area
+    long long a_first;      // where all replaced rows of the warp are of one head: their a0
+    uint32_t reps;          // the warp's rows that look their scores up
+    bool one_head;
+};
+
+// A block of a warp that is not plain: it has replaced rows, or keys that a row
+// does not see.  32 keys at a time, in a loop (a cold unrolled copy would cost more
+// to fetch than to run), the maximum kept as it goes: where it moves, what the
+// block has written of P so far is scaled along with O and l.  first: O holds
+// nothing yet.
+__device__ __noinline__ void mixed_block(RowState& st, const Patterns& w, bool keyed, bool first, uint32_t tS, uint32_t tO,
+                                         uint32_t tP, int k0, int len, uint32_t bad, int lb) {
+    const int lane = threadIdx.x & 31;
+    const bool rep = (w.reps >> lane) & 1u;
+    const int vis_last = max(st.vis, 1) - 1;
+    float m = st.m, l = st.l;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        if (keyed) {
+            tmem_ld32(tS + 32 * c, v);
+            tmem_wait_ld();
+        }
+        if (w.reps) {
+            const int key = k0 + 32 * c + lane;
+            const float av = w.one_head ? __ldg(w.a + w.a_first + min(key, len - 1)) : 0.f;
+#pragma unroll 4
+            for (int rr = 0; rr < 32; ++rr) {
+                if (!((w.reps >> rr) & 1u)) continue;
+                const int j = min(key, __shfl_sync(~0u, vis_last, rr));
+                const longlong2 at = w.rows[rr];
+                w.pat[rr * PAT_PITCH + lane] = (w.one_head ? av : __ldg(w.a + at.x + j)) + __ldg(w.r + at.y - j);
+            }
+            __syncwarp();
+            if (rep) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(w.pat[lane * PAT_PITCH + e]);
+            }
+            __syncwarp();
+        }
+        const int left = st.vis - k0 - 32 * c;
+        float mx2[2] = {kNegInf, kNegInf};
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = __float_as_uint(kNegInf);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+            mx2[(e >> 1) & 1] = max3(mx2[(e >> 1) & 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        const float mx = fmaxf(mx2[0], mx2[1]);
+        const bool grow = (mx - m) * st.unit > 8.f;
+        if (__any_sync(~0u, grow)) {
+            const float f = grow ? ex2((m - mx) * st.unit) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+            tmem_wait_st();
+            if (!first) rescale_o(tO, f);
+#pragma unroll 1
+            for (int d = 0; d < c; ++d) {
+                uint32_t pw[16];
+                tmem_ld16(tP + 16 * d, pw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    pw[e] = pack_bf16x2(__uint_as_float(pw[e] << 16) * f, __uint_as_float(pw[e] & 0xffff0000u) * f);
+                tmem_st16(tP + 16 * d, pw);
+            }
+            tmem_wait_st();
+        }
+        // (x - m) * unit, not x * unit - m * unit: a pattern's products may overflow where the difference is small
+        const float base = m == kNegInf ? 0.f : m;
+        const uint64_t base2 = f32x2(base, base), unit2 = f32x2(st.unit, st.unit);
+        uint64_t l2[2] = {0, 0};
+        uint32_t pw[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            const float2 x =
+                split_f32x2(mul_f32x2(sub_f32x2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), base2), unit2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], f32x2(p0, p1));
+            pw[e >> 1] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(tP + 16 * c, pw);
+        const float2 s2 = split_f32x2(add_f32x2(l2[0], l2[1]));
+        l += s2.x + s2.y;
+    }
+    st.m = m;
+    st.l = l;
+}
+
+template <bool PREFIX>
+__global__ void __launch_bounds__(NTHREADS, 2)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ PagedParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t bar_kf = sbase + SM_BAR, bar_ke = bar_kf + 8 * NST;  // [NST] K stage full, free (S MMA done)
+    const uint32_t bar_vf = bar_ke + 8 * NST, bar_ve = bar_vf + 8 * NST;  // [NST] V stage full, free (P V MMA done)
+    const uint32_t bar_s = bar_ve + 8 * NST;                            // S ready
+    const uint32_t bar_sf = bar_s + 8;                                  // S copied out by the rows (4 warp arrivals)
+    const uint32_t bar_p = bar_sf + 8;                                  // P written (4 warp arrivals)
+    const uint32_t bar_o = bar_p + 8;                                   // P V done
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SM_MISC);
+    volatile int* last_flag = reinterpret_cast<int*>(smem + SM_MISC + 4);
+    volatile uint32_t* meta = reinterpret_cast<uint32_t*>(smem + SM_MISC + 8);
+    int* warp_vis = reinterpret_cast<int*>(smem + SM_MISC + 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // row block (neighbouring CTAs share their keys), stretch, K/V head, sequence
+    int id = blockIdx.x;
+    const int rb = id % p.nrb;
+    id /= p.nrb;
+    const int split = id % p.splits;
+    id /= p.splits;
+    const int gi = id % p.Hkv, b = id / p.Hkv;
+    const int g = p.order[gi];
+    const bool keyed = gi < p.keyed;
+    const int len = key_len<PREFIX>(p, b), n_all = (len + BN - 1) / BN;
+    const int t0 = (int)((long long)split * n_all / p.splits), t_end = (int)((long long)(split + 1) * n_all / p.splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(bar_kf + 8 * s, 1);
+            mbar_init(bar_ke + 8 * s, 1);
+            mbar_init(bar_vf + 8 * s, 1);
+            mbar_init(bar_ve + 8 * s, 1);
+        }
+        mbar_init(bar_s, 1);
+        mbar_init(bar_sf, 4);
+        mbar_init(bar_p, 4);
+        mbar_init(bar_o, 1);
+        fence_mbar_init();
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_holder), TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (PREFIX) griddep_launch_dependents();  // the batch's own keys may start
+
+    // ---- the rows
+    const int quarter = warp & 3, row = quarter * 32 + lane;  // (row threads)
+    RowInfo info;
+    info.out = -1;
+    info.vis = info.replaced = 0;
+    if (warp >= 2) {
+        const int n = PREFIX ? 0 : new_tokens(p, b);
+        info = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, rb * BM + row);
+        const int most = __reduce_max_sync(~0u, info.vis);
+        if (lane == 0) warp_vis[quarter] = most;
+        reinterpret_cast<longlong2*>(smem + SM_ROW)[row] = make_longlong2(info.a0, info.r0);
+        if (keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(info.out, 0) * kHeadDim);
+            const bool read = info.out >= 0 && !info.replaced;
+            uint4 w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) w[c] = read ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                st_shared_v4(sbase + SM_Q + row * 128 + ((c ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+            fence_proxy_async_smem();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    // blocks that some row sees
+    const int most = max(max(warp_vis[0], warp_vis[1]), max(warp_vis[2], warp_vis[3]));
+    const int nt = max(0, min(t_end, (most + BN - 1) / BN) - t0);
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer
+        const int lp = p.log_page, lb = min(lp, 7);  // page and box rows
+        const uint32_t box_bytes = 128u << lb;
+        const int boxes = BN >> lb;
+        const int32_t* table = p.table + (size_t)b * p.table_stride;
+        bool ok = true;
+        int page = -1, loaded = -1;  // this lane's box of block `loaded`
+        bool need = false;
+        auto look_up = [&](int i) {
+            if (loaded == i) return;
+            loaded = i;
+            const int key = (t0 + i) * BN + (lane << lb);
+            need = lane < boxes && key < len;
+            page = need ? __ldg(table + (key >> lp)) : -1;
+        };
+        auto load = [&](int i, bool keys) {
+            look_up(i);
+            const int s = i & 1;
+            const uint32_t full = (keys ? bar_kf : bar_vf) + 8 * s, empty = (keys ? bar_ke : bar_ve) + 8 * s;
+            const bool good = need && page >= 0 && page < p.num_pages;
+            const uint32_t bad = __ballot_sync(~0u, lane < boxes && !good);
+            const int loads = __popc(__ballot_sync(~0u, good));
+            if (!mbar_wait_warp(empty, ((i >> 1) & 1) ^ 1, kWaitLimit)) return false;
+            if (lane == 0) {
+                if (!keys) meta[s] = bad;
+                mbar_expect_tx(full, loads * box_bytes);
+            }
+            __syncwarp();
+            if (good)
+                tma_load_4d(sbase + (keys ? SM_K : SM_V) + s * TILE_BYTES + lane * box_bytes, keys ? &tmK : &tmV, full, 0,
+                            ((t0 + i) * BN + (lane << lb)) & ((1 << lp) - 1), g, page);
+            return true;
+        };
+        // K runs a block ahead of V, as S runs ahead of P V
+        int issued_k = 0, issued_v = 0;
+        for (int i = 0; ok && i < nt; ++i) {
+            if (keyed && i == 0) ok = load(0, true), issued_k = 1;
+            if (ok) ok = load(i, false), issued_v = i + 1;
+            if (ok && keyed && i + 1 < nt) ok = load(i + 1, true), issued_k = i + 2;
+        }
+        if (!ok && lane == 0) {  // a wait gave up: the loads in flight land (or give up in turn) before the memory is let go
+            report(p.err, 0x501);
+            for (int i = max(0, issued_k - 2); i < issued_k - 1; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+            for (int i = max(0, issued_v - 2); i < issued_v - 1; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (see fwd_tc for the elected lane)
+        const uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q (K-major) x K (K-major)
+        const uint32_t idO = idesc_bf16(128, 64, 0, 1);   // P (TMEM) x V (MN-major)
+        constexpr uint64_t kStage = TILE_BYTES >> 4;
+        const uint64_t dQ = sw128_desc(sbase + SM_Q), dK0 = sw128_desc(sbase + SM_K), dV0 = sw128_desc(sbase + SM_V);
+        bool ok = true;
+        auto issue_s = [&](int i) {
+            const int s = i & 1;
+            if (!mbar_wait_warp(bar_kf + 8 * s, (i >> 1) & 1, kWaitLimit)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(tmem, dQ + 2 * k, dK0 + s * kStage + 2 * k, idS, k > 0 ? 1u : 0u);
+                mma_commit(bar_s);
+                mma_commit(bar_ke + 8 * s);
+            }
+            __syncwarp();
+            return true;
+        };
+        if (keyed && nt > 0) ok = issue_s(0);
+        for (int i = 0; ok && i < nt; ++i) {
+            if (keyed && i + 1 < nt) ok = mbar_wait_warp(bar_sf, i & 1, kWaitLimit) && issue_s(i + 1);
+            const int s = i & 1;
+            ok = ok && mbar_wait_warp(bar_vf + 8 * s, (i >> 1) & 1, kWaitLimit) && mbar_wait_warp(bar_p, i & 1, kWaitLimit);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(tmem + TO_COL, tmem + TP_COL + 8 * k, dV0 + s * kStage + 128 * k, idO, (i > 0 || k > 0) ? 1u : 0u);
+                mma_commit(bar_o);
+                mma_commit(bar_ve + 8 * s);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) report(p.err, 0x502);
+    } else {
+        // ------------------------------------------------ row threads
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + TO_COL, tP = tmem + lane_off + TP_COL;
+        const int lb = min(p.log_page, 7);
+        const bool rep = info.out >= 0 && info.replaced;
+        const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : INT_MAX);
+        RowState st{kNegInf, 0.f, rep ? kLog2e : 0.125f * kLog2e, info.vis};
+        Patterns pt;
+        pt.a = p.a;
+        pt.r = p.r;
+        pt.rows = reinterpret_cast<const longlong2*>(smem + SM_ROW) + quarter * 32;
+        pt.pat = reinterpret_cast<float*>(smem + SM_PAT) + quarter * 32 * PAT_PITCH;
+        pt.reps = __ballot_sync(~0u, rep && info.vis > 0);
+        pt.a_first = __shfl_sync(~0u, info.a0, pt.reps ? __ffs(pt.reps) - 1 : 0);
+        pt.one_head = __all_sync(~0u, !((pt.reps >> lane) & 1u) || info.a0 == pt.a_first);
+        bool ok = true;
+        for (int i = 0; i < nt; ++i) {
+            const int k0 = (t0 + i) * BN;
+            // V has landed: its pages are known
+            ok = mbar_wait_warp(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+            if (ok && keyed) ok = mbar_wait_warp(bar_s, i & 1, kWaitLimit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t bad = meta[i & 1];
+            if (pt.reps || k0 + BN > vmin || bad) {
+                if (i > 0) {  // P V of the block before has read P and added to O
+                    ok = mbar_wait_warp(bar_o, (i - 1) & 1, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                mixed_block(st, pt, keyed, i == 0, tS, tO, tP, k0, len, bad, lb);
+                if (keyed) {
+                    tc_fence_before();
+                    mbar_arrive_warp(bar_sf);
+                }
+            } else {
+                uint32_t v[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive_warp(bar_sf);  // the MMA warp may now overwrite S
+                const float mx = row_max(v);
+                float f = 1.f;
+                if ((mx - st.m) * st.unit > 8.f) {
+                    f = ex2((st.m - mx) * st.unit);
+                    st.l *= f;
+                    st.m = mx;
+                }
+                if (i > 0) {
+                    ok = mbar_wait_warp(bar_o, (i - 1) & 1, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const float nm = st.m == kNegInf ? 0.f : -st.m * st.unit;
+                const uint64_t unit2 = f32x2(st.unit, st.unit), nm2 = f32x2(nm, nm);
+                uint64_t l2[4] = {0, 0, 0, 0};
+                exp_quarter<0>(v, unit2, nm2, l2, tP);
+                exp_quarter<1>(v, unit2, nm2, l2, tP);
+                exp_quarter<2>(v, unit2, nm2, l2, tP);
+                exp_quarter<3>(v, unit2, nm2, l2, tP);
+                const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
+                st.l += s2.x + s2.y;
+                if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
+            }
+            if (k0 + BN > len || bad) {
+                // slots without a token may hold a NaN, and 0 times that is one: their V rows become zeros
+                if (k0 + row >= len || ((bad >> (row >> lb)) & 1u)) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) st_shared_v4(sbase + SM_V + (i & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive_warp(bar_p);
+        }
+        if (ok && nt > 0) ok = mbar_wait_warp(bar_o, (nt - 1) & 1, kWaitLimit);
+        if (!ok && lane == 0) report(p.err, 0x503);
+        tc_fence_after();
+        const float m = rep ? st.m : 0.125f * st.m, l = st.l;
+        if (!PREFIX && p.part) griddep_wait();
+        // ---- the rows out: a part of the prefix, a piece of several, or the output
+        const bool pieces = !PREFIX && p.splits > 1;
+        const size_t item = ((size_t)b * p.Hkv + gi) * p.nrb + rb;
+        float* slot = p.slots + (item * p.splits + split) * BM * (kHeadDim + 2);
+        float mo = m, lo = l;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t ov[32];
+            if (nt > 0) {
+                tmem_ld32(tO + 32 * c, ov);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                float4 o = make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                       __uint_as_float(ov[e + 3]));
+                const int col = 32 * c + e;
+                if (pieces) {
+                    __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + col), o);
+                } else if (info.out >= 0) {
+                    if (PREFIX) {
+                        *reinterpret_cast<float4*>(part_o(p, split, info.part) + col) = o;
+                    } else {
+                        mo = m;
+                        lo = l;
+                        if (p.part) join_parts(p, info.part, col, o, mo, lo);
+                        store_row(p, info, col, o, mo, lo);
+                    }
+                }
+            }
+        }
+        if (PREFIX && info.out >= 0) store_part_ml(p, split, info.part, m, l);
+        if (pieces) {
+            __stcg(slot + BM * kHeadDim + row, m);
+            __stcg(slot + BM * (kHeadDim + 1) + row, l);
+            __threadfence();
+            named_sync(1, 128);
+            if (row == 0) *last_flag = atomicAdd(p.counters + item, 1u) == (unsigned)p.splits - 1;
+            named_sync(1, 128);
+            if (*last_flag) {
+                __threadfence();
+                const float* first = p.slots + item * p.splits * BM * (kHeadDim + 2);
+                constexpr int STRIDE = BM * (kHeadDim + 2);
+                const int n = new_tokens(p, b);
+                const int c = (row & 15) * 4;
+                for (int rr = row >> 4; rr < BM; rr += 8) {
+                    const RowInfo x = row_info<false>(p, b, g, len, n, p.prefix_len + len - n, rb * BM + rr);
+                    if (x.out < 0) continue;  // alike in the sixteen threads of a row
+                    float mm = kNegInf;
+                    for (int k = 0; k < p.splits; ++k) mm = fmaxf(mm, __ldcg(first + (size_t)k * STRIDE + BM * kHeadDim + rr));
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float ll = 0.f;
+#pragma unroll 4
+                    for (int k = 0; k < p.splits; ++k) {
+                        const float* sl = first + (size_t)k * STRIDE;
+                        const float fk = weight(__ldcg(sl + BM * kHeadDim + rr), mm);
+                        const float4 w = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c));
+                        o = make_float4(o.x + fk * w.x, o.y + fk * w.y, o.z + fk * w.z, o.w + fk * w.w);
+                        ll += fk * __ldcg(sl + BM * (kHeadDim + 1) + rr);
+                    }
+                    if (p.part) join_parts(p, x.part, c, o, mm, ll);
+                    store_row(p, x, c, o, mm, ll);
+                }
+                if (row == 0) atomicExch(p.counters + item, 0u);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <bool PREFIX>
+cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStream_t stream) {
+    CUtensorMap mk, mv;
+    if (!make_tmap_pages(kv, true, BN, &mk) || !make_tmap_pages(kv, false, BN, &mv)) return cudaErrorNotSupported;
+    p.nrb = (p.rows + BM - 1) / BM;
+    p.by_T = divisor(p.T);
+    p.by_R = divisor(p.R);
+    const double ctas = (double)p.nseq * p.Hkv * p.nrb * p.splits;
+    if (ctas >= 2147483648.0) return cudaErrorNotSupported;
+    const int smem = SM_TOTAL + 1024;
+    cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    const int kid = PREFIX ? KID_PAGED_PREFIX_TC : KID_PAGED_TC;
+    launch_begin(kid, stream);
+    e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<PREFIX>, mk, mv, p);
+    launch_end(kid, stream);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Stretches of the keys: the fewest waves of CTAs (two per SM) times blocks per
+// CTA, an item's own cost counted as four blocks.
+int tc_splits(int items, int max_keys) {
+    const int tiles = std::max(1, (max_keys + BN - 1) / BN);
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= tiles && (s == 1 || (int64_t)items * s <= kTcCtas); ++s) {
+        const double waves = (double)(((int64_t)items * s + 295) / 296);
+        const double cost = waves * ((tiles + s - 1) / s + 4);
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, bool overlap, cudaStream_t stream) {
+    return prefix ? launch<true>(kv, p, overlap, stream) : launch<false>(kv, p, overlap, stream);
+}
+
+}  // namespace saf
