@@ -255,21 +255,22 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             }
             const int g = p.order[w.gi], row0 = w.rb * ROWS;
             x.rows = min(ROWS, p.rows - row0);
+            int out;
             {  // a lane per row
                 const int n = PREFIX ? 0 : new_tokens(p, b);
                 const RowInfo row = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, row0 + lane);
                 x.replaced = __ballot_sync(~0u, lane < x.rows && row.replaced && row.vis > 0);
                 x.vmin = __reduce_min_sync(~0u, lane < x.rows && row.out >= 0 ? row.vis : INT_MAX);
+                out = row.out;
                 if (lane < ROWS) *reinterpret_cast<RowInfo*>(smem + L::INFO + (slot * ROWS + lane) * sizeof(RowInfo)) = row;
             }
             if (lane == 0) *reinterpret_cast<Piece*>(smem + L::ITEM + 48 * slot) = x;
             __syncwarp();
             if (lane == 0) mbar_expect_tx(bar_item + 8 * slot, x.rows * 128);
             __syncwarp();
-            if (lane < x.rows) {  // the queries
-                const int rr = row0 + lane, qb = PREFIX ? p.by_R.div(rr) : b, rem = PREFIX ? rr - qb * p.R : rr;
-                bulk_load(sbase + L::Q + (slot * ROWS + lane) * Q_PITCH,
-                          p.q + (((size_t)qb * p.H + g * p.G) * p.T + rem) * kHeadDim, 128, bar_item + 8 * slot);
+            if (lane < x.rows) {  // the queries, a row that has no token taking row 0's
+                bulk_load(sbase + L::Q + (slot * ROWS + lane) * Q_PITCH, p.q + (size_t)max(out, 0) * kHeadDim, 128,
+                          bar_item + 8 * slot);
             }
             const int tk = w.keyed ? TK : 2 * TK, boxes = tk >> lb;
             const int32_t* table = p.table + (size_t)b * p.table_stride;
@@ -724,7 +725,7 @@ cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, Page
     const int per = block_rows(p.rows);
     p.nrb = (p.rows + per - 1) / per;
     p.by_T = divisor(p.T);
-    p.by_R = divisor(p.R);
+    p.by_BT = divisor(p.B * p.T);
     p.by_nrb = divisor(p.nrb);
     // all units in 31 bits
     const double most = kItem + std::max(1, (std::max(p.max_len, p.prefix_len) + TK - 1) / TK);
@@ -773,6 +774,10 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
             if (c.keyless.get(g) == (want == 1)) p.order[n++] = (uint8_t)g;
         if (want == 0) p.keyed = n;
     }
+    for (int g = 0, at = 0; g < p.Hkv; ++g)
+        for (int want = 0; want < 2; ++want)
+            for (int h = g * p.G; h < (g + 1) * p.G; ++h)
+                if (c.replaced.get(h) == (want == 1)) p.heads[at++] = (uint8_t)h;
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
         p.part = reinterpret_cast<float*>(c.ws + w.part);

@@ -58,7 +58,7 @@ struct RowInfo {
     long long a0, r0;
     int vis;        // keys it sees
     int out, part;  // its row of the output (-1: it has no token), and of the prefix's parts
-    int replaced;
+    int replaced;   // its head + 1, or 0
 };
 
 // Division by a launch constant: n / d = (umulhi(n, m) + n) >> s for 0 <= n < 2^31, with 2^(s-1) < d <= 2^s and
@@ -87,9 +87,10 @@ struct PagedParams {
     int table_stride, num_pages, log_page, Hkv;
     int B, H, T, G, R, max_len;  // R = G T rows of one (b, g)
     int nseq, rows, nrb;         // key sequences, rows of one item list entry, row blocks
-    Divisor by_T, by_R, by_nrb;
+    Divisor by_T, by_BT, by_nrb;
     int keyed;                   // K/V heads with keys: the first of order[]
     uint8_t order[kMaxHeads];    // K/V heads, those with keys first
+    uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
     // What the prefix came to (or null): [parts][Hkv * B * R][64] O, then [parts][Hkv * B * R] m, and the same of l.
@@ -121,8 +122,10 @@ __device__ __forceinline__ int key_len(const PagedParams& p, int b) {
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
     return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
 }
-// Row rr of the item list entry (b, g); n, pos0: the sequence's new tokens and
-// the position of the first (with PREFIX they are looked up per row).
+// Row rr of the item list entry (b, g), head by head (the ordinary heads of the
+// group first): with PREFIX (head, sequence, token), else (head, token) of sequence b.  n, pos0: the
+// sequence's new tokens and the position of the first (with PREFIX they are
+// looked up per row).
 template <bool PREFIX>
 __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int g, int len, int n, int pos0, int rr) {
     RowInfo x;
@@ -131,8 +134,9 @@ __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int g, 
     x.out = -1;
     x.replaced = 0;
     if (rr >= p.rows) return x;
-    const int rb = PREFIX ? p.by_R.div(rr) : b, rem = PREFIX ? rr - rb * p.R : rr;
-    const int u = p.by_T.div(rem), h = g * p.G + u, t = rem - u * p.T;
+    const int u = (PREFIX ? p.by_BT : p.by_T).div(rr), h = p.heads[g * p.G + u];
+    const int rem = rr - u * (PREFIX ? p.B * p.T : p.T);
+    const int rb = PREFIX ? p.by_T.div(rem) : b, t = PREFIX ? rem - rb * p.T : rem;
     if (PREFIX) {
         n = new_tokens(p, rb);
         pos0 = p.prefix_len + key_len<false>(p, rb) - n;
@@ -144,8 +148,8 @@ __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int g, 
     x.a0 = ph + key_base;
     x.r0 = ph + pos0 + t - key_base;
     x.out = (rb * p.H + h) * p.T + t;
-    x.part = (g * p.B + rb) * p.R + rem;
-    x.replaced = p.replaced.get(h);
+    x.part = ((g * p.G + u) * p.B + rb) * p.T + t;
+    x.replaced = p.replaced.get(h) ? h + 1 : 0;
     return x;
 }
 

@@ -14,9 +14,13 @@
 //               2^-8 off, as in the layer's forward), the sum in fp32
 // S_{j+1} is issued as soon as the rows have copied S_j to registers, before P V_j.
 //   ordinary row   s = q . k / 8
-//   replaced row   s = a[j] + r[i - j]: 32 keys at a time, a warp reads each of its
-//                  replaced rows' stretch of r side by side (lane = key) into shared
-//                  memory and every thread takes its own row from there
+//   replaced row   s = a[j] + r[i - j], 32 keys at a time: a thread reads its own stretch
+//                  of r where the warp's stretches lie together (a chunk's tokens, or
+//                  sequences of one length), else the warp copies the rows' stretches to
+//                  shared memory side by side, asynchronously and 16 bytes at a time, and
+//                  every thread takes its row from there
+// Rows come head by head, a group's ordinary heads first, so that most warps hold
+// one kind, and blocks of replaced rows alone need no K.
 // With a prefix each stretch is a part that the batch's own keys are joined to;
 // otherwise a row of one stretch is written at once, and of several by the CTA that
 // finishes the row block's last one, in key order.
@@ -43,11 +47,17 @@ constexpr long long kWaitLimit = 1ll << 31;
 constexpr uint32_t SM_Q = 0;
 constexpr uint32_t SM_K = SM_Q + TILE_BYTES;
 constexpr uint32_t SM_V = SM_K + NST * TILE_BYTES;
-constexpr int PAT_PITCH = 33;                               // floats: a warp's reads of its 32 rows hit distinct banks
-constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;        // [4 warps][32 rows][PAT_PITCH]
-constexpr uint32_t SM_ROW = SM_PAT + 4 * 32 * PAT_PITCH * 4;  // [128] {a0, r0} of a row
-constexpr uint32_t SM_BAR = SM_ROW + 128 * 16;
-constexpr uint32_t SM_MISC = SM_BAR + 16 * 8;  // TMEM address, last flag, [2] boxes without a page, [4] largest vis of a row warp
+constexpr int PAT_PITCH = 33;                          // floats: a warp's reads of its 32 rows hit distinct banks
+// Stretches of 16 keys of 32 rows of r, from the 16-byte boundary at or before them on: 20 floats a row, three buffers
+constexpr int FAR_PITCH = 20, FAR_BUF = 32 * FAR_PITCH, FAR_BUFS = 3;
+constexpr uint32_t PAT_BYTES = FAR_BUFS * FAR_BUF * 4;  // a warp's staging area
+static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4, "both uses fit");
+constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;   // [4 warps] staging area
+constexpr uint32_t SM_A = SM_PAT + 4 * PAT_BYTES;      // [4 warps][32] a of 32 keys
+constexpr uint32_t SM_ROW = SM_A + 4 * 32 * 4;         // [128] {head, r at local key 0 within the head's} of a row
+constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
+// TMEM address, last flag, [2] boxes without a page, [4] largest vis of a row warp, [4] whether it has an ordinary row
+constexpr uint32_t SM_MISC = SM_BAR + 16 * 8;
 constexpr uint32_t SM_TOTAL = SM_MISC + 64;
 
 // Row max of 128 raw scores: three-input max, four independent chains.
@@ -88,103 +98,212 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
     }
 }
 
-// What a row thread keeps between blocks, and what it looks scores up by.
-struct RowState {
-    float m, l;  // running maximum (in units of the row's scores), sum
-    float unit;  // log2(e) per unit: dot products are 8 of a score
-    int vis;
-};
+// What a warp's rows look scores up by.
 struct Patterns {
-    const float *a, *r;
-    const longlong2* rows;  // {a0, r0} of the warp's rows
-    float* pat;             // the warp's staging area
-    long long a_first;      // where all replaced rows of the warp are of one head: their a0
-    uint32_t reps;          // the warp's rows that look their scores up
-    bool one_head;
+    const float *a, *r;    // of the head of the warp's first replaced row, at local key 0 (r: at its own position, pr[-j])
+    const float *a0, *r0;  // the arrays, a0 at local key 0 of head 0
+    int pattern_len;
+    const int2* rows;  // {head, r at local key 0 within the head's} of the warp's rows
+    float *pat, *aw;   // the warp's staging areas
+    uint32_t reps;     // the warp's rows that look their scores up
+    bool one_head;     // all of these are of one head
 };
 
-// A block of a warp that is not plain: it has replaced rows, or keys that a row
-// does not see.  32 keys at a time, in a loop (a cold unrolled copy would cost more
-// to fetch than to run), the maximum kept as it goes: where it moves, what the
-// block has written of P so far is scaled along with O and l.  first: O holds
-// nothing yet.
-__device__ __noinline__ void mixed_block(RowState& st, const Patterns& w, bool keyed, bool first, uint32_t tS, uint32_t tO,
-                                         uint32_t tP, int k0, int len, uint32_t bad, int lb) {
+// Scores of 32 keys, chunk c of a block, of a row each: the maximum moves if it
+// must (then what the block has written of P so far is scaled along with O and
+// l), P goes to TMEM and its sum to l.  first: O holds nothing yet.
+__device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool first, float unit, float& m, float& l,
+                                          uint32_t tO, uint32_t tP) {
+    float mx2[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) mx2[(e >> 1) & 1] = max3(mx2[(e >> 1) & 1], v[e], v[e + 1]);
+    const float mx = fmaxf(mx2[0], mx2[1]);
+    const bool grow = (mx - m) * unit > 8.f;
+    if (__any_sync(~0u, grow)) {
+        const float f = grow ? ex2((m - mx) * unit) : 1.f;
+        if (grow) m = mx;
+        l *= f;
+        tmem_wait_st();
+        if (!first) rescale_o(tO, f);
+#pragma unroll 1
+        for (int d = 0; d < c; ++d) {
+            uint32_t pw[16];
+            tmem_ld16(tP + 16 * d, pw);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                pw[e] = pack_bf16x2(__uint_as_float(pw[e] << 16) * f, __uint_as_float(pw[e] & 0xffff0000u) * f);
+            tmem_st16(tP + 16 * d, pw);
+        }
+        tmem_wait_st();
+    }
+    // (x - m) * unit, not x * unit - m * unit: a pattern's products may overflow where the difference is small
+    const float base = m == kNegInf ? 0.f : m;
+    const uint64_t base2 = f32x2(base, base), unit2 = f32x2(unit, unit);
+    uint64_t l2[2] = {0, 0};
+    uint32_t pw[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 x = split_f32x2(mul_f32x2(sub_f32x2(f32x2(v[e], v[e + 1]), base2), unit2));
+        const float p0 = ex2(x.x), p1 = ex2(x.y);
+        l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], f32x2(p0, p1));
+        pw[e >> 1] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(tP + 16 * c, pw);
+    const float2 s2 = split_f32x2(add_f32x2(l2[0], l2[1]));
+    l += s2.x + s2.y;
+}
+
+// a of the 32 keys from `key` on, to every thread through the warp's staging area.
+__device__ __forceinline__ void add_a(float (&v)[32], const Patterns& w, float mine) {
     const int lane = threadIdx.x & 31;
-    const bool rep = (w.reps >> lane) & 1u;
-    const int vis_last = max(st.vis, 1) - 1;
-    float m = st.m, l = st.l;
+    w.aw[lane] = mine;
+    __syncwarp();
+    const float4* ap = reinterpret_cast<const float4*>(w.aw);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 av = ap[e >> 2];
+        v[e] += av.x;
+        v[e + 1] += av.y;
+        v[e + 2] += av.z;
+        v[e + 3] += av.w;
+    }
+    __syncwarp();
+}
+
+// A block of a warp whose rows are all replaced, of one head, and see every key of
+// it, their stretches of r within a few lines of each other (so that a load of all
+// lanes touches few).  off: this thread's row against w.r.  Returns (m, l).
+__device__ __noinline__ float2 near_block(float m, float l, const Patterns& w, bool first, int off, uint32_t tO, uint32_t tP,
+                                          int k0) {
+    const int lane = threadIdx.x & 31;
+    const float *rp = w.r + off - k0, *ap = w.a + k0 + lane;
+    float nx[32], na = __ldg(ap);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) nx[e] = __ldg(rp - e);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = nx[e];
+        const float mine = na;
+        if (c < 3) {
+            rp -= 32;
+            ap += 32;
+            na = __ldg(ap);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) nx[e] = __ldg(rp - e);
+        }
+        add_a(v, w, mine);
+        chunk_out(v, c, first, kLog2e, m, l, tO, tP);
+    }
+    return make_float2(m, l);
+}
+
+// The same where they lie anywhere: 16 keys at a time by asynchronous copies, three
+// under way.  src[i]: where this lane's i-th 16 bytes of the stretch from local key 0 on
+// lie against w.r (rows 8 i + lane / 4; src[4]: the fifth of its own row, with the
+// floats of r that are left from there on in `room`); shift: floats between the
+// boundary and the row's stretch.  primed: the block's first copies are under way;
+// next: the block after it is of this kind, its first copies are started.
+struct FarRows {
+    int src[5];
+    int shift;
+    long long room;
+};
+__device__ __forceinline__ void far_copy(const Patterns& w, const FarRows& f, int key) {  // the 16 keys from `key` on
+    const int lane = threadIdx.x & 31;
+    const uint32_t buf = smem_addr(w.pat) + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF * 4;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const uint32_t dst = buf + (i < 4 ? (8 * i + (lane >> 2)) * FAR_PITCH + 4 * (lane & 3) : lane * FAR_PITCH + 16) * 4;
+        // the fifth may end past the array's last float, or begin there (a stretch that starts on a boundary needs none)
+        const int bytes = i < 4 ? 16 : (int)min(16ll, max(0ll, (f.room + key) * 4));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(w.r + f.src[i] - key), "r"(bytes));
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+__device__ __noinline__ float2 far_block(float m, float l, const Patterns& w, const FarRows& f, bool primed, bool next,
+                                         bool first, uint32_t tO, uint32_t tP, int k0) {
+    const int lane = threadIdx.x & 31;
+    if (!primed) {
+#pragma unroll 1
+        for (int n = 0; n < FAR_BUFS; ++n) far_copy(w, f, k0 + 16 * n);
+    }
+    float na = __ldg(w.a + k0 + lane);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float v[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = 2 * c + h, key = k0 + 16 * n;
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(FAR_BUFS - 1) : "memory");
+            __syncwarp();
+            const float* src = w.pat + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF + lane * FAR_PITCH + f.shift + 15;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[16 * h + e] = src[-e];
+            __syncwarp();
+            if (n + FAR_BUFS < 8 || next) far_copy(w, f, key + 16 * FAR_BUFS);
+            else asm volatile("cp.async.commit_group;\n" ::: "memory");
+        }
+        const float mine = na;
+        if (c < 3) na = __ldg(w.a + k0 + 32 * (c + 1) + lane);
+        add_a(v, w, mine);
+        chunk_out(v, c, first, kLog2e, m, l, tO, tP);
+    }
+    return make_float2(m, l);
+}
+
+// A block of a warp that is neither that nor plain: it holds both kinds, or there are
+// keys that a row does not see.  32 keys at a time, in a loop (a cold unrolled
+// copy would cost more to fetch than to run).  Returns (m, l).
+__device__ __noinline__ float2 mixed_block(float m, float l, const Patterns& w, float unit, int vis, bool keyed, bool first,
+                                           uint32_t tS, uint32_t tO, uint32_t tP, int k0, int len, uint32_t bad, int lb) {
+    const int lane = threadIdx.x & 31;
+    const bool rep = (w.reps >> lane) & 1u;
+    const int vis_last = max(vis, 1) - 1;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t raw[32];
+        float v[32];
         if (keyed) {
-            tmem_ld32(tS + 32 * c, v);
+            tmem_ld32(tS + 32 * c, raw);
             tmem_wait_ld();
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
         if (w.reps) {
             const int key = k0 + 32 * c + lane;
-            const float av = w.one_head ? __ldg(w.a + w.a_first + min(key, len - 1)) : 0.f;
-#pragma unroll 4
-            for (int rr = 0; rr < 32; ++rr) {
-                if (!((w.reps >> rr) & 1u)) continue;
-                const int j = min(key, __shfl_sync(~0u, vis_last, rr));
-                const longlong2 at = w.rows[rr];
-                w.pat[rr * PAT_PITCH + lane] = (w.one_head ? av : __ldg(w.a + at.x + j)) + __ldg(w.r + at.y - j);
+            const float av = w.one_head ? __ldg(w.a + min(key, len - 1)) : 0.f;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                if (!((w.reps >> r0) & 0xffu)) continue;
+                float x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {  // (a row that looks nothing up reads entry 0)
+                    const int j = min(key, __shfl_sync(~0u, vis_last, r0 + u));
+                    const int2 at = w.rows[r0 + u];
+                    const bool read = (w.reps >> (r0 + u)) & 1u;
+                    const long long ph = (long long)at.x * w.pattern_len;
+                    x[u] = (w.one_head ? av : __ldg(read ? w.a0 + ph + j : w.a)) + __ldg(read ? w.r0 + ph + at.y - j : w.r);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) w.pat[(r0 + u) * PAT_PITCH + lane] = x[u];
             }
             __syncwarp();
             if (rep) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(w.pat[lane * PAT_PITCH + e]);
+                for (int e = 0; e < 32; ++e) v[e] = w.pat[lane * PAT_PITCH + e];
             }
             __syncwarp();
         }
-        const int left = st.vis - k0 - 32 * c;
-        float mx2[2] = {kNegInf, kNegInf};
+        const int left = vis - k0 - 32 * c;
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = __float_as_uint(kNegInf);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-            mx2[(e >> 1) & 1] = max3(mx2[(e >> 1) & 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        const float mx = fmaxf(mx2[0], mx2[1]);
-        const bool grow = (mx - m) * st.unit > 8.f;
-        if (__any_sync(~0u, grow)) {
-            const float f = grow ? ex2((m - mx) * st.unit) : 1.f;
-            if (grow) m = mx;
-            l *= f;
-            tmem_wait_st();
-            if (!first) rescale_o(tO, f);
-#pragma unroll 1
-            for (int d = 0; d < c; ++d) {
-                uint32_t pw[16];
-                tmem_ld16(tP + 16 * d, pw);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    pw[e] = pack_bf16x2(__uint_as_float(pw[e] << 16) * f, __uint_as_float(pw[e] & 0xffff0000u) * f);
-                tmem_st16(tP + 16 * d, pw);
-            }
-            tmem_wait_st();
-        }
-        // (x - m) * unit, not x * unit - m * unit: a pattern's products may overflow where the difference is small
-        const float base = m == kNegInf ? 0.f : m;
-        const uint64_t base2 = f32x2(base, base), unit2 = f32x2(st.unit, st.unit);
-        uint64_t l2[2] = {0, 0};
-        uint32_t pw[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            const float2 x =
-                split_f32x2(mul_f32x2(sub_f32x2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), base2), unit2));
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
-            l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], f32x2(p0, p1));
-            pw[e >> 1] = pack_bf16x2(p0, p1);
-        }
-        tmem_st16(tP + 16 * c, pw);
-        const float2 s2 = split_f32x2(add_f32x2(l2[0], l2[1]));
-        l += s2.x + s2.y;
+            if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = kNegInf;
+        chunk_out(v, c, first, unit, m, l, tO, tP);
     }
-    st.m = m;
-    st.l = l;
+    return make_float2(m, l);
 }
 
 template <bool PREFIX>
@@ -203,7 +322,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SM_MISC);
     volatile int* last_flag = reinterpret_cast<int*>(smem + SM_MISC + 4);
     volatile uint32_t* meta = reinterpret_cast<uint32_t*>(smem + SM_MISC + 8);
-    int* warp_vis = reinterpret_cast<int*>(smem + SM_MISC + 16);
+    int *warp_vis = reinterpret_cast<int*>(smem + SM_MISC + 16), *warp_keyed = warp_vis + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // row block (neighbouring CTAs share their keys), stretch, K/V head, sequence
@@ -214,7 +333,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     id /= p.splits;
     const int gi = id % p.Hkv, b = id / p.Hkv;
     const int g = p.order[gi];
-    const bool keyed = gi < p.keyed;
     const int len = key_len<PREFIX>(p, b), n_all = (len + BN - 1) / BN;
     const int t0 = (int)((long long)split * n_all / p.splits), t_end = (int)((long long)(split + 1) * n_all / p.splits);
 
@@ -248,9 +366,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int n = PREFIX ? 0 : new_tokens(p, b);
         info = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, rb * BM + row);
         const int most = __reduce_max_sync(~0u, info.vis);
-        if (lane == 0) warp_vis[quarter] = most;
-        reinterpret_cast<longlong2*>(smem + SM_ROW)[row] = make_longlong2(info.a0, info.r0);
-        if (keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
+        const int ordinary = __any_sync(~0u, info.out >= 0 && !info.replaced);
+        if (lane == 0) {
+            warp_vis[quarter] = most;
+            warp_keyed[quarter] = ordinary;
+        }
+        const int head = max(info.replaced - 1, 0);
+        reinterpret_cast<int2*>(smem + SM_ROW)[row] = make_int2(head, (int)(info.r0 - (long long)head * p.pattern_len));
+        if (gi < p.keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
             const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(info.out, 0) * kHeadDim);
             const bool read = info.out >= 0 && !info.replaced;
             uint4 w[8];
@@ -269,6 +392,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // blocks that some row sees
     const int most = max(max(warp_vis[0], warp_vis[1]), max(warp_vis[2], warp_vis[3]));
     const int nt = max(0, min(t_end, (most + BN - 1) / BN) - t0);
+    const bool keyed = warp_keyed[0] | warp_keyed[1] | warp_keyed[2] | warp_keyed[3];  // the block reads K
 
     if (warp == 0) {
         // ------------------------------------------------ producer
@@ -361,15 +485,38 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int lb = min(p.log_page, 7);
         const bool rep = info.out >= 0 && info.replaced;
         const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : INT_MAX);
-        RowState st{kNegInf, 0.f, rep ? kLog2e : 0.125f * kLog2e, info.vis};
+        const float unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
         Patterns pt;
-        pt.a = p.a;
-        pt.r = p.r;
-        pt.rows = reinterpret_cast<const longlong2*>(smem + SM_ROW) + quarter * 32;
-        pt.pat = reinterpret_cast<float*>(smem + SM_PAT) + quarter * 32 * PAT_PITCH;
         pt.reps = __ballot_sync(~0u, rep && info.vis > 0);
-        pt.a_first = __shfl_sync(~0u, info.a0, pt.reps ? __ffs(pt.reps) - 1 : 0);
-        pt.one_head = __all_sync(~0u, !((pt.reps >> lane) & 1u) || info.a0 == pt.a_first);
+        const bool looks = (pt.reps >> lane) & 1u;
+        const int from = pt.reps ? __ffs(pt.reps) - 1 : 0;
+        const long long a_first = __shfl_sync(~0u, info.a0, from), r_first = __shfl_sync(~0u, info.r0, from);
+        pt.a = p.a + a_first;
+        pt.r = p.r + r_first;
+        pt.a0 = p.a + (PREFIX ? 0 : p.prefix_len);
+        pt.r0 = p.r;
+        pt.pattern_len = p.pattern_len;
+        pt.rows = reinterpret_cast<const int2*>(smem + SM_ROW) + quarter * 32;
+        pt.pat = reinterpret_cast<float*>(smem + SM_PAT + quarter * PAT_BYTES);
+        pt.aw = reinterpret_cast<float*>(smem + SM_A) + quarter * 32;
+        pt.one_head = __all_sync(~0u, !looks || info.a0 == a_first);
+        // all rows with a token look up, by one head's vectors: the others ride along on the first one's
+        const bool pure = pt.reps && pt.one_head && __all_sync(~0u, info.out < 0 || looks);
+        const int off = looks && pt.one_head ? (int)(info.r0 - r_first) : 0;  // (within a head's vector)
+        const bool near = __all_sync(~0u, off < 64 && off > -64);
+        FarRows far;
+        bool primed = false;
+        if (pure && !near) {
+            // the stretch of the 16 keys from key k on begins 15 floats before r's entry of key k
+            const long long start = r_first + off - 15;
+            const int edge = (int)((start & ~3ll) - r_first);
+            far.shift = (int)(start & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) far.src[i] = __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3);
+            far.src[4] = edge + 16;
+            far.room = (long long)p.H * p.pattern_len - (r_first + edge + 16);
+        }
+        float m = kNegInf, l = 0.f;  // running maximum (in the row's units), sum
         bool ok = true;
         for (int i = 0; i < nt; ++i) {
             const int k0 = (t0 + i) * BN;
@@ -385,7 +532,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     if (!ok) break;
                     tc_fence_after();
                 }
-                mixed_block(st, pt, keyed, i == 0, tS, tO, tP, k0, len, bad, lb);
+                float2 ml;
+                if (pure && k0 + BN <= vmin && !bad) {
+                    if (near) {
+                        ml = near_block(m, l, pt, i == 0, off, tO, tP, k0);
+                    } else {
+                        const bool next = i + 1 < nt && k0 + 2 * BN <= vmin;
+                        ml = far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
+                        primed = next;
+                    }
+                } else {
+                    if (primed) {  // copies begun for this block: its staging area is wanted
+                        asm volatile("cp.async.wait_all;\n" ::: "memory");
+                        __syncwarp();
+                        primed = false;
+                    }
+                    ml = mixed_block(m, l, pt, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, len, bad, lb);
+                }
+                m = ml.x;
+                l = ml.y;
                 if (keyed) {
                     tc_fence_before();
                     mbar_arrive_warp(bar_sf);
@@ -399,25 +564,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 mbar_arrive_warp(bar_sf);  // the MMA warp may now overwrite S
                 const float mx = row_max(v);
                 float f = 1.f;
-                if ((mx - st.m) * st.unit > 8.f) {
-                    f = ex2((st.m - mx) * st.unit);
-                    st.l *= f;
-                    st.m = mx;
+                if ((mx - m) * unit > 8.f) {
+                    f = ex2((m - mx) * unit);
+                    l *= f;
+                    m = mx;
                 }
                 if (i > 0) {
                     ok = mbar_wait_warp(bar_o, (i - 1) & 1, kWaitLimit);
                     if (!ok) break;
                     tc_fence_after();
                 }
-                const float nm = st.m == kNegInf ? 0.f : -st.m * st.unit;
-                const uint64_t unit2 = f32x2(st.unit, st.unit), nm2 = f32x2(nm, nm);
+                const float nm = m == kNegInf ? 0.f : -m * unit;
+                const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
                 uint64_t l2[4] = {0, 0, 0, 0};
                 exp_quarter<0>(v, unit2, nm2, l2, tP);
                 exp_quarter<1>(v, unit2, nm2, l2, tP);
                 exp_quarter<2>(v, unit2, nm2, l2, tP);
                 exp_quarter<3>(v, unit2, nm2, l2, tP);
                 const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
-                st.l += s2.x + s2.y;
+                l += s2.x + s2.y;
                 if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
             }
             if (k0 + BN > len || bad) {
@@ -432,10 +597,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             tc_fence_before();
             mbar_arrive_warp(bar_p);
         }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
         if (ok && nt > 0) ok = mbar_wait_warp(bar_o, (nt - 1) & 1, kWaitLimit);
         if (!ok && lane == 0) report(p.err, 0x503);
         tc_fence_after();
-        const float m = rep ? st.m : 0.125f * st.m, l = st.l;
+        if (!rep) m *= 0.125f;
         if (!PREFIX && p.part) griddep_wait();
         // ---- the rows out: a part of the prefix, a piece of several, or the output
         const bool pieces = !PREFIX && p.splits > 1;
@@ -521,7 +687,7 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStr
     if (!make_tmap_pages(kv, true, BN, &mk) || !make_tmap_pages(kv, false, BN, &mv)) return cudaErrorNotSupported;
     p.nrb = (p.rows + BM - 1) / BM;
     p.by_T = divisor(p.T);
-    p.by_R = divisor(p.R);
+    p.by_BT = divisor(p.B * p.T);
     const double ctas = (double)p.nseq * p.Hkv * p.nrb * p.splits;
     if (ctas >= 2147483648.0) return cudaErrorNotSupported;
     const int smem = SM_TOTAL + 1024;
