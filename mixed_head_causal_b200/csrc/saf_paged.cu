@@ -276,12 +276,12 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const int32_t* table = p.table + (size_t)b * p.table_stride;
             const int npages = (x.len + (1 << lp) - 1) >> lp;
             int ids = -1, ids0 = -64;  // page ids [ids0, ids0 + 32), one per lane
-            for (int t = x.t0; t < x.t1; ++t, ++it) {
+            for (int t = x.t1 - 1; t >= x.t0; --t, ++it) {  // last tile first (see the consumers)
                 const int s = it % NS, key = t * tk + (lane << lb);  // this lane's box
                 const int pg_lo = (t * tk) >> lp, pg_hi = (t * tk + tk - 1) >> lp;
                 if (pg_lo < ids0 || pg_hi >= ids0 + 32) {
-                    ids0 = pg_lo;
-                    ids = pg_lo + lane < npages ? __ldg(table + pg_lo + lane) : -1;
+                    ids0 = max(0, pg_hi - 31);
+                    ids = ids0 + lane < npages ? __ldg(table + ids0 + lane) : -1;
                 }
                 const int page = __shfl_sync(~0u, ids, ((key >> lp) - ids0) & 31);
                 const bool need = lane < boxes && key < x.len;
@@ -380,7 +380,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         // The warps' turns: a tile with K and V goes to one warp, one of V alone to two.
         const int turns = x.keyed ? NCW : NCW / 2, turn = x.keyed ? warp : warp >> 1, sub = x.keyed ? 0 : warp & 1;
         const int tk = x.keyed ? TK : 2 * TK;
-        int t = x.t0 + ((turn - it) & (turns - 1));
+        // Last tile first: patterns tend to favour near keys, so that the running maximum starts near where it ends.
+        int t = x.t1 - 1 - ((turn - it) & (turns - 1));
         // A replaced row's scores of 64 keys are summed lane by lane (two each) into the warp's part of `red`, and
         // read back in the fragment's order.  The first such row's are loaded a step ahead; the others of the same
         // head then find theirs in L1.
@@ -389,22 +390,22 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const RowInfo& w = info[__ffs(x.replaced) - 1];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = min(key + lane + 32 * e, w.vis - 1);
+                const int j = max(0, min(key + lane + 32 * e, w.vis - 1));
                 ahead[e] = __ldg(p.a + w.a0 + j);
                 ahead[2 + e] = __ldg(p.r + w.r0 - j);
             }
         };
         if (x.replaced) load_ahead(t * tk + sub * TK);
 
-        for (; t < x.t1; t += turns) {
-            const unsigned at = (unsigned)(it + t - x.t0), s = at % NS;
+        for (; t >= x.t0; t -= turns) {
+            const unsigned at = (unsigned)(it + x.t1 - 1 - t), s = at % NS;
             const int k0 = t * tk + sub * TK;
             const uint32_t sk = sbase + s * STAGE, sv = sk + (x.keyed || sub ? HALF : 0);
             if (x.replaced) {
                 const int first = __ffs(x.replaced) - 1;
                 mine[first * RED_PITCH + lane] = ahead[0] + ahead[2];
                 mine[first * RED_PITCH + lane + 32] = ahead[1] + ahead[3];
-                load_ahead(k0 + turns * tk);
+                load_ahead(k0 - turns * tk);
                 for (uint32_t left = x.replaced & (x.replaced - 1); left; left &= left - 1) {
                     const int row = __ffs(left) - 1;
                     const RowInfo& w = info[row];

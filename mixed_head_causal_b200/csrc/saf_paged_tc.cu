@@ -3,7 +3,8 @@
 //
 // A CTA takes 128 rows of one K/V head (its query heads times the new tokens, and
 // with a shared prefix times the sequences) and one stretch of their keys, in
-// blocks of 128.  Two CTAs per SM, six warps each:
+// blocks of 128, last block first (patterns tend to favour near keys: the running
+// maximum then starts near where it ends).  Two CTAs per SM, six warps each:
 //   warp 0      producer: page look-up and TMA loads, a box per page, two stages each
 //               of K and V (no K for a K/V head whose query heads are all replaced)
 //   warp 1      TMEM owner and MMA issuer (one elected lane):
@@ -48,13 +49,15 @@ constexpr uint32_t SM_Q = 0;
 constexpr uint32_t SM_K = SM_Q + TILE_BYTES;
 constexpr uint32_t SM_V = SM_K + NST * TILE_BYTES;
 constexpr int PAT_PITCH = 33;                          // floats: a warp's reads of its 32 rows hit distinct banks
-// Stretches of 16 keys of 32 rows of r, from the 16-byte boundary at or before them on: 20 floats a row, three buffers
-constexpr int FAR_PITCH = 20, FAR_BUF = 32 * FAR_PITCH, FAR_BUFS = 3;
+// A staging area holds three buffers of 16 keys: the stretches of 32 rows of r, from the 16-byte boundary at or
+// before them on (20 floats a row), and a; or two of 128 keys: a, and r from the first to the last row's; or (mixed
+// blocks) the scores of 32 keys of 32 rows.
+constexpr int FAR_PITCH = 20, FAR_A = 32 * FAR_PITCH, FAR_BUF = FAR_A + 16, FAR_BUFS = 3;
+constexpr int NEAR_SPAN = 64, NEAR_BUF = 128 + 128 + NEAR_SPAN;  // floats; rows at most NEAR_SPAN apart
 constexpr uint32_t PAT_BYTES = FAR_BUFS * FAR_BUF * 4;  // a warp's staging area
-static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4, "both uses fit");
+static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4 && PAT_BYTES >= 2 * NEAR_BUF * 4, "all uses fit");
 constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;   // [4 warps] staging area
-constexpr uint32_t SM_A = SM_PAT + 4 * PAT_BYTES;      // [4 warps][32] a of 32 keys
-constexpr uint32_t SM_ROW = SM_A + 4 * 32 * 4;         // [128] {head, r at local key 0 within the head's} of a row
+constexpr uint32_t SM_ROW = SM_PAT + 4 * PAT_BYTES;  // [128] {head, r at local key 0 within the head's} of a row
 constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
 // TMEM address, last flag, [2] boxes without a page, [4] largest vis of a row warp, [4] whether it has an ordinary row
 constexpr uint32_t SM_MISC = SM_BAR + 16 * 8;
@@ -104,14 +107,16 @@ struct Patterns {
     const float *a0, *r0;  // the arrays, a0 at local key 0 of head 0
     int pattern_len;
     const int2* rows;  // {head, r at local key 0 within the head's} of the warp's rows
-    float *pat, *aw;   // the warp's staging areas
+    float* pat;        // the warp's staging area
     uint32_t reps;     // the warp's rows that look their scores up
+    int span;          // from the lowest of their stretches of r to the highest
     bool one_head;     // all of these are of one head
 };
 
-// Scores of 32 keys, chunk c of a block, of a row each: the maximum moves if it
-// must (then what the block has written of P so far is scaled along with O and
-// l), P goes to TMEM and its sum to l.  first: O holds nothing yet.
+// Scores of 32 keys, chunk c of a block (which goes from 3 to 0), of a row each:
+// the maximum moves if it must (then what the block has written of P so far is
+// scaled along with O and l), P goes to TMEM and its sum to l.  first: O holds
+// nothing yet.
 __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool first, float unit, float& m, float& l,
                                           uint32_t tO, uint32_t tP) {
     float mx2[2] = {kNegInf, kNegInf};
@@ -126,7 +131,7 @@ __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool firs
         tmem_wait_st();
         if (!first) rescale_o(tO, f);
 #pragma unroll 1
-        for (int d = 0; d < c; ++d) {
+        for (int d = c + 1; d < 4; ++d) {
             uint32_t pw[16];
             tmem_ld16(tP + 16 * d, pw);
             tmem_wait_ld();
@@ -154,58 +159,62 @@ __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool firs
     l += s2.x + s2.y;
 }
 
-// a of the 32 keys from `key` on, to every thread through the warp's staging area.
-__device__ __forceinline__ void add_a(float (&v)[32], const Patterns& w, float mine) {
-    const int lane = threadIdx.x & 31;
-    w.aw[lane] = mine;
-    __syncwarp();
-    const float4* ap = reinterpret_cast<const float4*>(w.aw);
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// v[e] += a[e], read by all lanes alike
+template <int N>
+__device__ __forceinline__ void add_a(float* v, const float* a) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        const float4 av = ap[e >> 2];
+    for (int e = 0; e < N; e += 4) {
+        const float4 av = *reinterpret_cast<const float4*>(a + e);
         v[e] += av.x;
         v[e + 1] += av.y;
         v[e + 2] += av.z;
         v[e + 3] += av.w;
     }
-    __syncwarp();
 }
 
 // A block of a warp whose rows are all replaced, of one head, and see every key of
-// it, their stretches of r within a few lines of each other (so that a load of all
-// lanes touches few).  off: this thread's row against w.r.  Returns (m, l).
-__device__ __noinline__ float2 near_block(float m, float l, const Patterns& w, bool first, int off, uint32_t tO, uint32_t tP,
-                                          int k0) {
+// it, their stretches of r at most NEAR_SPAN apart: one stretch serves them all,
+// copied a block ahead.  low: the lowest row's offset against w.r, off: this one's
+// against that.  primed: the block's copies are under way; next: the block after it
+// is of this kind, and its copies are started.  Returns (m, l).
+__device__ __forceinline__ void near_copy(const Patterns& w, int low, int k0) {
     const int lane = threadIdx.x & 31;
-    const float *rp = w.r + off - k0, *ap = w.a + k0 + lane;
-    float nx[32], na = __ldg(ap);
+    const uint32_t buf = smem_addr(w.pat) + (uint32_t)((k0 / BN) & 1) * NEAR_BUF * 4;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) nx[e] = __ldg(rp - e);
+    for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, w.a + k0 + 32 * i + lane);
+    const float* r = w.r + low - k0 - 127;  // r of the lowest row's last key
+#pragma unroll
+    for (int i = 0; i < (128 + NEAR_SPAN) / 32; ++i) copy4(buf + (128 + 32 * i + lane) * 4, r + min(32 * i + lane, w.span + 127));
+    copies_commit();
+}
+__device__ __noinline__ float2 near_block(float m, float l, const Patterns w, bool primed, bool next, bool first, int low,
+                                          int off, uint32_t tO, uint32_t tP, int k0) {
+    if (!primed) near_copy(w, low, k0);
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
+    if (next) near_copy(w, low, k0 - BN);
+    const float *a = w.pat + ((k0 / BN) & 1) * NEAR_BUF, *r = a + 128 + 127 + off;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 3; c >= 0; --c) {
         float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = nx[e];
-        const float mine = na;
-        if (c < 3) {
-            rp -= 32;
-            ap += 32;
-            na = __ldg(ap);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) nx[e] = __ldg(rp - e);
-        }
-        add_a(v, w, mine);
+        for (int e = 0; e < 32; ++e) v[e] = r[-32 * c - e];
+        add_a<32>(v, a + 32 * c);
         chunk_out(v, c, first, kLog2e, m, l, tO, tP);
     }
+    __syncwarp();  // the buffer has been read
     return make_float2(m, l);
 }
 
-// The same where they lie anywhere: 16 keys at a time by asynchronous copies, three
-// under way.  src[i]: where this lane's i-th 16 bytes of the stretch from local key 0 on
-// lie against w.r (rows 8 i + lane / 4; src[4]: the fifth of its own row, with the
-// floats of r that are left from there on in `room`); shift: floats between the
-// boundary and the row's stretch.  primed: the block's first copies are under way;
-// next: the block after it is of this kind, its first copies are started.
+// The same where they lie anywhere: 16 keys at a time, three under way.  src[i]:
+// where this lane's i-th 16 bytes of the stretch from local key 0 on lie against
+// w.r (rows 8 i + lane / 4; src[4]: the fifth of its own row, with the floats of r
+// that are left from there on in `room`); shift: floats between the boundary and
+// the row's stretch.
 struct FarRows {
     int src[5];
     int shift;
@@ -221,34 +230,33 @@ __device__ __forceinline__ void far_copy(const Patterns& w, const FarRows& f, in
         const int bytes = i < 4 ? 16 : (int)min(16ll, max(0ll, (f.room + key) * 4));
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(w.r + f.src[i] - key), "r"(bytes));
     }
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    if (lane < 16) copy4(buf + (FAR_A + lane) * 4, w.a + key + lane);
+    copies_commit();
 }
-__device__ __noinline__ float2 far_block(float m, float l, const Patterns& w, const FarRows& f, bool primed, bool next,
+__device__ __noinline__ float2 far_block(float m, float l, const Patterns w, const FarRows f, bool primed, bool next,
                                          bool first, uint32_t tO, uint32_t tP, int k0) {
     const int lane = threadIdx.x & 31;
     if (!primed) {
 #pragma unroll 1
-        for (int n = 0; n < FAR_BUFS; ++n) far_copy(w, f, k0 + 16 * n);
+        for (int n = 7; n > 7 - FAR_BUFS; --n) far_copy(w, f, k0 + 16 * n);
     }
-    float na = __ldg(w.a + k0 + lane);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 3; c >= 0; --c) {
         float v[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 1; h >= 0; --h) {
             const int n = 2 * c + h, key = k0 + 16 * n;
             asm volatile("cp.async.wait_group %0;\n" ::"n"(FAR_BUFS - 1) : "memory");
             __syncwarp();
-            const float* src = w.pat + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF + lane * FAR_PITCH + f.shift + 15;
+            const float* buf = w.pat + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF;
+            const float* src = buf + lane * FAR_PITCH + f.shift + 15;
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[16 * h + e] = src[-e];
+            add_a<16>(v + 16 * h, buf + FAR_A);
             __syncwarp();
-            if (n + FAR_BUFS < 8 || next) far_copy(w, f, key + 16 * FAR_BUFS);
-            else asm volatile("cp.async.commit_group;\n" ::: "memory");
+            if (n >= FAR_BUFS || next) far_copy(w, f, key - 16 * FAR_BUFS);
+            else copies_commit();
         }
-        const float mine = na;
-        if (c < 3) na = __ldg(w.a + k0 + 32 * (c + 1) + lane);
-        add_a(v, w, mine);
         chunk_out(v, c, first, kLog2e, m, l, tO, tP);
     }
     return make_float2(m, l);
@@ -257,13 +265,13 @@ __device__ __noinline__ float2 far_block(float m, float l, const Patterns& w, co
 // A block of a warp that is neither that nor plain: it holds both kinds, or there are
 // keys that a row does not see.  32 keys at a time, in a loop (a cold unrolled
 // copy would cost more to fetch than to run).  Returns (m, l).
-__device__ __noinline__ float2 mixed_block(float m, float l, const Patterns& w, float unit, int vis, bool keyed, bool first,
+__device__ __noinline__ float2 mixed_block(float m, float l, const Patterns w, float unit, int vis, bool keyed, bool first,
                                            uint32_t tS, uint32_t tO, uint32_t tP, int k0, int len, uint32_t bad, int lb) {
     const int lane = threadIdx.x & 31;
     const bool rep = (w.reps >> lane) & 1u;
     const int vis_last = max(vis, 1) - 1;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 3; c >= 0; --c) {
         uint32_t raw[32];
         float v[32];
         if (keyed) {
@@ -406,7 +414,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         auto look_up = [&](int i) {
             if (loaded == i) return;
             loaded = i;
-            const int key = (t0 + i) * BN + (lane << lb);
+            const int key = (t0 + nt - 1 - i) * BN + (lane << lb);
             need = lane < boxes && key < len;
             page = need ? __ldg(table + (key >> lp)) : -1;
         };
@@ -425,7 +433,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             __syncwarp();
             if (good)
                 tma_load_4d(sbase + (keys ? SM_K : SM_V) + s * TILE_BYTES + lane * box_bytes, keys ? &tmK : &tmV, full, 0,
-                            ((t0 + i) * BN + (lane << lb)) & ((1 << lp) - 1), g, page);
+                            ((t0 + nt - 1 - i) * BN + (lane << lb)) & ((1 << lp) - 1), g, page);
             return true;
         };
         // K runs a block ahead of V, as S runs ahead of P V
@@ -498,12 +506,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         pt.pattern_len = p.pattern_len;
         pt.rows = reinterpret_cast<const int2*>(smem + SM_ROW) + quarter * 32;
         pt.pat = reinterpret_cast<float*>(smem + SM_PAT + quarter * PAT_BYTES);
-        pt.aw = reinterpret_cast<float*>(smem + SM_A) + quarter * 32;
         pt.one_head = __all_sync(~0u, !looks || info.a0 == a_first);
         // all rows with a token look up, by one head's vectors: the others ride along on the first one's
         const bool pure = pt.reps && pt.one_head && __all_sync(~0u, info.out < 0 || looks);
         const int off = looks && pt.one_head ? (int)(info.r0 - r_first) : 0;  // (within a head's vector)
-        const bool near = __all_sync(~0u, off < 64 && off > -64);
+        const int low = __reduce_min_sync(~0u, off);
+        pt.span = __reduce_max_sync(~0u, off) - low;
+        const bool near = pt.span <= NEAR_SPAN;
         FarRows far;
         bool primed = false;
         if (pure && !near) {
@@ -519,7 +528,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         float m = kNegInf, l = 0.f;  // running maximum (in the row's units), sum
         bool ok = true;
         for (int i = 0; i < nt; ++i) {
-            const int k0 = (t0 + i) * BN;
+            const int k0 = (t0 + nt - 1 - i) * BN;
             // V has landed: its pages are known
             ok = mbar_wait_warp(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
             if (ok && keyed) ok = mbar_wait_warp(bar_s, i & 1, kWaitLimit);
@@ -534,13 +543,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
                 float2 ml;
                 if (pure && k0 + BN <= vmin && !bad) {
-                    if (near) {
-                        ml = near_block(m, l, pt, i == 0, off, tO, tP, k0);
-                    } else {
-                        const bool next = i + 1 < nt && k0 + 2 * BN <= vmin;
-                        ml = far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
-                        primed = next;
-                    }
+                    const bool next = i + 1 < nt;
+                    ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off - low, tO, tP, k0)
+                              : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
+                    primed = next;
                 } else {
                     if (primed) {  // copies begun for this block: its staging area is wanted
                         asm volatile("cp.async.wait_all;\n" ::: "memory");
