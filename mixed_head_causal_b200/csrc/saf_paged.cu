@@ -43,8 +43,9 @@ using mma::mma_bf16;
 
 constexpr int TK = 64;               // keys per tile with K and V (twice as many of V alone)
 constexpr int CTAS_PER_SM = 2;
-constexpr int kMaxGrid = 1024;       // bounds the workspace
-constexpr int kItem = 4, kSnap = 4, kMinUnits = 8;
+struct SplitAxis {
+    static constexpr int kTile = TK, kTileKeyless = 2 * TK, kItem = 4, kSnap = 4, kMinUnits = 8;
+};
 constexpr int kMaxBlocks = 4;        // row blocks of eight that one item holds
 constexpr uint32_t HALF = TK * 128;  // bytes of a tile's K or V
 constexpr uint32_t STAGE = 2 * HALF;
@@ -88,41 +89,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Tiles of an item (one without keys still takes one, empty, tile: its rows are written).
-__device__ __forceinline__ int tiles_of(int len, bool keyed) {
-    const int tk = keyed ? TK : 2 * TK;
-    return max(1, (len + tk - 1) / tk);
-}
-// Units of a sequence on the axis.
-__device__ __forceinline__ int seq_units(const PagedParams& p, int len) {
-    return p.nrb * (p.keyed * (tiles_of(len, true) + kItem) + (p.Hkv - p.keyed) * (tiles_of(len, false) + kItem));
-}
-
-// The item that unit u of sequence b is in (base: the sequence's first unit).
-struct Item {
-    int gi, rb, n, start;  // its tiles, its first unit
-    bool keyed;
-};
-__device__ __forceinline__ Item item_at(const PagedParams& p, int base, int len, int u) {
-    Item x;
-    int off = u - base;
-    x.n = tiles_of(len, true);
-    const int keyed_units = p.keyed * p.nrb * (x.n + kItem);
-    x.keyed = off < keyed_units;
-    int first = 0;
-    if (!x.keyed) {
-        x.n = tiles_of(len, false);
-        off -= keyed_units;
-        first = p.keyed;
-    }
-    const int block = (int)((unsigned)off / (unsigned)(x.n + kItem));  // K/V head and row block
-    x.gi = p.by_nrb.div(block);
-    x.rb = block - x.gi * p.nrb;
-    x.gi += first;
-    x.start = u - (off - block * (x.n + kItem));
-    return x;
-}
-
 template <int NB, bool PREFIX>
 __global__ void __launch_bounds__(32 * (Smem<NB>::NCW + 1), CTAS_PER_SM)
 paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -163,53 +129,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 
     if (warp == NCW) {
         // ------------------------------------------------ producer
-        // The CTA's stretch: each lane sums the units of a run of sequences.
-        const int chunk = (p.nseq + 31) >> 5, b_lo = min(lane * chunk, p.nseq), b_hi = min(b_lo + chunk, p.nseq);
-        int mine = 0;
-#pragma unroll 4
-        for (int b = b_lo; b < b_hi; ++b) mine += seq_units(p, key_len<PREFIX>(p, b));
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const int total = __shfl_sync(~0u, incl, 31), before = incl - mine;
-        // Stretch c begins at unit c * per + min(c, more): `more` stretches of per + 1 units, then those of `per`.
-        const int ctas = max(1, min((int)gridDim.x, total / kMinUnits)), cta = blockIdx.x;
-        const int per = (int)((unsigned)total / (unsigned)ctas), more = total - per * ctas;
-        const int lo = cta < ctas ? cta * per + min(cta, more) : total, hi = lo + per + (cta < more ? 1 : 0);
-        // The sequence of a unit below `total`, and its first unit.
-        auto find = [&](int u, int& b, int& base) {
-            const int src = __ffs(__ballot_sync(~0u, u >= before && u < before + mine)) - 1;
-            int at = before, bb = b_lo;
-            if (lane == src)
-                for (;; ++bb) {
-                    const int n = seq_units(p, key_len<PREFIX>(p, bb));
-                    if (u < at + n) break;
-                    at += n;
-                }
-            b = __shfl_sync(~0u, bb, src);
-            base = __shfl_sync(~0u, at, src);
-        };
-        int b = 0, base = 0, b_end = 0, base_end = 0;
-        if (lo < total) find(lo, b, base);
-        if (lo < total && hi < total) find(hi, b_end, base_end);
-        int len = key_len<PREFIX>(p, b);
-        // stretch ends close to an item's end move there
-        auto snapped = [&](int u, int bu, int base_u) {
-            const Item x = item_at(p, base_u, key_len<PREFIX>(p, bu), u);
-            const int stop = x.start + kItem + x.n;
-            return u - x.start <= kItem + kSnap ? x.start : stop - u <= kSnap ? stop : u;
-        };
-        int u = lo < total ? snapped(lo, b, base) : total;
-        const int end = hi < total ? snapped(hi, b_end, base_end) : total;
-        // The first stretch that begins at unit x > 0 or later.
-        auto first_from = [&](int x) {
-            const int big = more * (per + 1);
-            return x <= big ? (int)((unsigned)(x + per) / (unsigned)(per + 1))
-                            : more + (int)((unsigned)(x - big + per - 1) / (unsigned)per);
-        };
+        AxisWalk<SplitAxis, PREFIX> walk(p, blockIdx.x, gridDim.x);
         const int lp = p.log_page, lb = min(lp, 6);  // page and box rows
         const uint32_t box_bytes = 128u << lb;
         int it = 0;
@@ -222,24 +142,15 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         };
         for (int ni = 0;; ++ni) {
             Piece x;
-            Item w;
+            Stretch w;
             x.t1 = -1;  // no more
-            if (u < end) {
-                while (u >= base + seq_units(p, len)) {
-                    base += seq_units(p, len);
-                    len = key_len<PREFIX>(p, ++b);
-                }
-                w = item_at(p, base, len, u);
-                x.len = len;
+            if (walk.next(w)) {
+                x.len = w.len;
                 x.keyed = w.keyed;
-                x.t0 = max(0, u - w.start - kItem);
-                x.t1 = min(w.n, end - w.start - kItem);
-                // the stretches that begin strictly inside the item (see snapped())
-                const int in_lo = w.start + kItem + kSnap + 1, in_hi = w.start + kItem + w.n - kSnap;
-                const int c1 = in_lo < in_hi ? first_from(in_lo) : 0, c2 = in_lo < in_hi ? first_from(in_hi) : 0;
-                x.pieces = c2 - c1 + 1;
-                x.c_first = c1 - 1;
-                u = w.start + kItem + x.t1;
+                x.t0 = w.t0;
+                x.t1 = w.t1;
+                x.pieces = w.pieces;
+                x.c_first = w.c_first;
             }
             const int slot = ni % NI;
             if (!mbar_wait_warp(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1, kWaitLimit)) {
@@ -257,8 +168,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             x.rows = min(ROWS, p.rows - row0);
             int out;
             {  // a lane per row
-                const int n = PREFIX ? 0 : new_tokens(p, b);
-                const RowInfo row = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, row0 + lane);
+                const int n = PREFIX ? 0 : new_tokens(p, w.b);
+                const RowInfo row = row_info<PREFIX>(p, w.b, w.gi, w.len, n, p.prefix_len + w.len - n, row0 + lane);
                 x.replaced = __ballot_sync(~0u, lane < x.rows && row.replaced && row.vis > 0);
                 x.vmin = __reduce_min_sync(~0u, lane < x.rows && row.out >= 0 ? row.vis : INT_MAX);
                 out = row.out;
@@ -273,7 +184,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                           bar_item + 8 * slot);
             }
             const int tk = w.keyed ? TK : 2 * TK, boxes = tk >> lb;
-            const int32_t* table = p.table + (size_t)b * p.table_stride;
+            const int32_t* table = p.table + (size_t)w.b * p.table_stride;
             const int npages = (x.len + (1 << lp) - 1) >> lp;
             int ids = -1, ids0 = -64;  // page ids [ids0, ids0 + 32), one per lane
             for (int t = x.t1 - 1; t >= x.t0; --t, ++it) {  // last tile first (see the consumers)
@@ -326,17 +237,6 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             if (!ok && lane == 0) report(p.err, 0x405);
         }
         ++joins;
-    };
-    // A finished row (four columns from c): with PREFIX the part that the batch's own keys are joined to.
-    auto finish = [&](const RowInfo& row, int c, float4 acc, float mm, float ll) {
-        if (row.out < 0) return;
-        if (PREFIX) {
-            *reinterpret_cast<float4*>(part_o(p, 0, row.part) + c) = acc;
-            if (c == 0) store_part_ml(p, 0, row.part, mm, ll);
-        } else {
-            if (p.part) join_parts(p, row.part, c, acc, mm, ll);
-            store_row(p, row, c, acc, mm, ll);
-        }
     };
     for (int ni = 0;; ++ni) {
         if (ok) {
@@ -596,7 +496,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
         join_warps();
         const int c = (tid & 15) * 4;
-        if (!PREFIX && p.part && !waited) {
+        if (!PREFIX && p.prefix.part && !waited) {
             griddep_wait();
             waited = true;
         }
@@ -615,7 +515,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 ll += f * red_l[k * ROWS + row];
             }
             if (x.pieces == 1) {
-                finish(info[row], c, acc, mm, ll);
+                finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + c), acc);
                 if (c == 0) {
@@ -649,7 +549,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                         acc = make_float4(acc.x + f * v.x, acc.y + f * v.y, acc.z + f * v.z, acc.w + f * v.w);
                         ll += f * __ldcg(sl + ROWS * (kHeadDim + 1) + row);
                     }
-                    finish(info[row], c, acc, mm, ll);
+                    finish_row<PREFIX>(p, info[row], c, acc, mm, ll);
                 }
                 if (tid == 0) atomicExch(p.counters + x.c_first, 0u);
             }
@@ -667,9 +567,8 @@ int block_rows(int rows) { return ((rows + row_blocks(rows) - 1) / row_blocks(ro
 // Items of more rows than this go to the tensor-core kernel.
 constexpr int kTcRows = 32;
 
-// Workspace: header, the two launches' piece counters, the pieces of the one
-// that joins them, the prefix's parts.  Sizes bound every choice of kernel and
-// split, so that they grow with each argument.
+// Workspace: header, the two launches' piece counters and pieces, the prefix's
+// parts.  Sizes grow with each argument.
 struct PagedWs {
     size_t counters[2], slots[2], part, total;
 };
@@ -681,17 +580,13 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
         w.counters[k] = off;
         off += kMaxGrid * sizeof(unsigned int);
     }
-    auto split_slots = [](int64_t rows) { return 2 * kMaxGrid * std::min<int64_t>(8 * kMaxBlocks, (rows + 7) & ~7ll); };
-    auto tc_rows = [](int64_t items) { return 128 * (kTcCtas + items); };  // items * splits <= kTcCtas + items
     for (int k = 0; k < (prefix_len > 0 ? 2 : 1); ++k) {
+        const int rows = k ? B * R : R, most = rows > kTcRows ? 128 : (rows + 7) & ~7;
         w.slots[k] = off;
-        const int64_t rows = k ? (int64_t)B * R : R;
-        int64_t need = split_slots(rows);
-        if (k == 0 && rows > kTcRows) need = std::max<int64_t>(need, tc_rows(std::min(kTcCtas, tc_items(B, H_kv, R))));
-        off = align256(off + sizeof(float) * (size_t)need * (kHeadDim + 2));
+        off = align256(off + sizeof(float) * 2 * kMaxGrid * most * (kHeadDim + 2));
     }
     w.part = off;
-    if (prefix_len > 0) off = align256(off + sizeof(float) * (size_t)tc_rows(tc_items(1, H_kv, B * R)) * (kHeadDim + 2));
+    if (prefix_len > 0) off = align256(off + sizeof(float) * (size_t)B * H * T * (kHeadDim + 2));
     w.total = off;
     return w;
 }
@@ -703,7 +598,7 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
                                          (int)Smem<NB>::TOTAL);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min(kMaxGrid, CTAS_PER_SM * sm_count()));
+    cfg.gridDim = dim3((unsigned)paged_grid());
     cfg.blockDim = dim3(32 * (Smem<NB>::NCW + 1));
     cfg.dynamicSmemBytes = Smem<NB>::TOTAL;
     cfg.stream = stream;
@@ -728,9 +623,7 @@ cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, Page
     p.by_T = divisor(p.T);
     p.by_BT = divisor(p.B * p.T);
     p.by_nrb = divisor(p.nrb);
-    // all units in 31 bits
-    const double most = kItem + std::max(1, (std::max(p.max_len, p.prefix_len) + TK - 1) / TK);
-    if (most * p.nrb * p.Hkv * p.nseq >= 2147483648.0) return cudaErrorNotSupported;
+    if (!axis_fits<SplitAxis>(p)) return cudaErrorNotSupported;
     switch (per / 8) {
         case 1: return launch_split<1, PREFIX>(mk, mv, p, overlap, stream);
         case 2: return launch_split<2, PREFIX>(mk, mv, p, overlap, stream);
@@ -781,18 +674,16 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
                 if (c.replaced.get(h) == (want == 1)) p.heads[at++] = (uint8_t)h;
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
-        p.part = reinterpret_cast<float*>(c.ws + w.part);
+        p.prefix.part = reinterpret_cast<float*>(c.ws + w.part);
+        p.prefix.nrows = c.B * c.H * c.T;
         p.table = c.prefix_table;
         p.table_stride = 0;
         p.nseq = 1;
         p.rows = c.B * p.R;
         p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[1]);
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
-        const bool tc = p.rows > kTcRows;
-        p.splits = tc ? tc_splits(tc_items(1, p.Hkv, p.rows), c.prefix_len) : 1;
-        p.parts = p.splits;
-        const cudaError_t e = tc ? launch_paged_tc(c.kv, p, true, false, stream)
-                                 : launch_split_rows<true>(mk, mv, p, false, stream);
+        const cudaError_t e = p.rows > kTcRows ? launch_paged_tc(c.kv, p, true, false, stream)
+                                               : launch_split_rows<true>(mk, mv, p, false, stream);
         if (e != cudaSuccess) return e;
     }
     p.table = c.page_table;
@@ -802,7 +693,6 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
     if (p.rows <= kTcRows) return launch_split_rows<false>(mk, mv, p, c.prefix_len > 0, stream);
-    p.splits = tc_splits(tc_items(c.B, p.Hkv, p.rows), c.max_len);
     return launch_paged_tc(c.kv, p, false, c.prefix_len > 0, stream);
 }
 

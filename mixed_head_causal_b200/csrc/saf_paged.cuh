@@ -75,6 +75,25 @@ inline Divisor divisor(int d) {
     return x;
 }
 
+// A row's (m, l, O) before the division, of a block of rows: [rows][64] O, then m, then l.
+struct RowsRef {
+    const float *o, *m, *l;
+};
+// What the prefix came to, for the kernel of the batch's own keys: rows in the
+// order K/V head (by order[]), head of the group, sequence, token.  Rows of an item
+// that one CTA held whole are in `part` (all rows); the tensor-core kernel leaves
+// the others' in its CTAs' slots, to be joined where they are wanted (pieces of one
+// item by one CTA: 50 us for 16 items of 18 pieces).  part null: no prefix.
+struct PrefixParts {
+    float* part;
+    int nrows;          // all rows
+    const float* slots;  // null: everything is in `part`
+    int slot_floats;
+    int per, more, units, tiles, item_units, snap, nrb;  // the launch's axis, see AxisWalk
+    Divisor by_rows;    // rows of a K/V head
+    int rows;
+};
+
 // What the attention kernels need, by value.
 struct PagedParams {
     const __nv_bfloat16* q;
@@ -93,10 +112,7 @@ struct PagedParams {
     uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
-    // What the prefix came to (or null): [parts][Hkv * B * R][64] O, then [parts][Hkv * B * R] m, and the same of l.
-    float* part;
-    int parts;
-    int splits;                  // tensor-core kernel: stretches of the keys
+    PrefixParts prefix;
 };
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int code) {
@@ -122,19 +138,19 @@ __device__ __forceinline__ int key_len(const PagedParams& p, int b) {
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
     return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
 }
-// Row rr of the item list entry (b, g), head by head (the ordinary heads of the
+// Row rr of the item list entry (b, K/V head order[gi]), head by head (the ordinary heads of the
 // group first): with PREFIX (head, sequence, token), else (head, token) of sequence b.  n, pos0: the
 // sequence's new tokens and the position of the first (with PREFIX they are
 // looked up per row).
 template <bool PREFIX>
-__device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int g, int len, int n, int pos0, int rr) {
+__device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int gi, int len, int n, int pos0, int rr) {
     RowInfo x;
     x.a0 = x.r0 = 0;
     x.vis = x.part = 0;
     x.out = -1;
     x.replaced = 0;
     if (rr >= p.rows) return x;
-    const int u = (PREFIX ? p.by_BT : p.by_T).div(rr), h = p.heads[g * p.G + u];
+    const int u = (PREFIX ? p.by_BT : p.by_T).div(rr), h = p.heads[p.order[gi] * p.G + u];
     const int rem = rr - u * (PREFIX ? p.B * p.T : p.T);
     const int rb = PREFIX ? p.by_T.div(rem) : b, t = PREFIX ? rem - rb * p.T : rem;
     if (PREFIX) {
@@ -148,39 +164,56 @@ __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int g, 
     x.a0 = ph + key_base;
     x.r0 = ph + pos0 + t - key_base;
     x.out = (rb * p.H + h) * p.T + t;
-    x.part = ((g * p.G + u) * p.B + rb) * p.T + t;
+    x.part = ((gi * p.G + u) * p.B + rb) * p.T + t;
     x.replaced = p.replaced.get(h) ? h + 1 : 0;
     return x;
 }
 
-// What a finished row is joined with: the parts of the prefix.  M: the largest
-// maximum; weight(part's m, M) scales a part.
-__device__ __forceinline__ size_t part_rows(const PagedParams& p) { return (size_t)p.Hkv * p.B * p.R; }
-__device__ __forceinline__ const float* part_m(const PagedParams& p, int k, int row) {
-    return p.part + part_rows(p) * kHeadDim * p.parts + (size_t)k * part_rows(p) + row;
+// Stretch boundaries of an axis (see AxisWalk): the first stretch that begins at
+// unit x > 0 or later.
+__device__ __forceinline__ int first_from(int per, int more, int x) {
+    const int big = more * (per + 1);
+    return x <= big ? (int)((unsigned)(x + per) / (unsigned)(per + 1))
+                    : more + (int)((unsigned)(x - big + per - 1) / (unsigned)per);
 }
-__device__ __forceinline__ float* part_o(const PagedParams& p, int k, int row) {
-    return p.part + ((size_t)k * part_rows(p) + row) * kHeadDim;
+// The CTAs that share the item that begins at unit `start`: how many, and the
+// first (where there are several).
+__device__ __forceinline__ int pieces_of(int per, int more, int item_units, int snap, int start, int tiles, int& c_first) {
+    // the stretches that begin strictly inside the item, by more than a snap
+    const int in_lo = start + item_units + snap + 1, in_hi = start + item_units + tiles - snap;
+    const int c1 = in_lo < in_hi ? first_from(per, more, in_lo) : 0, c2 = in_lo < in_hi ? first_from(per, more, in_hi) : 0;
+    c_first = c1 - 1;
+    return c2 - c1 + 1;
 }
-__device__ __forceinline__ void store_part_ml(const PagedParams& p, int k, int row, float m, float l) {
-    float* pm = const_cast<float*>(part_m(p, k, row));
-    pm[0] = m;
-    pm[part_rows(p) * p.parts] = l;
-}
-// Four columns of a row (from c) joined with the prefix's parts: o, m and l are updated.
-__device__ __forceinline__ void join_parts(const PagedParams& p, int row, int c, float4& o, float& m, float& l) {
+// Four columns of a row (from c) joined with what the prefix came to: o, m and l are updated.
+__device__ __forceinline__ void join_prefix(const PagedParams& p, int row, int c, float4& o, float& m, float& l) {
+    const PrefixParts& x = p.prefix;
+    int pieces = 1, c_first = 0, in_block = 0;
+    if (x.slots) {
+        const int gi = x.by_rows.div(row), rr = row - gi * x.rows;
+        in_block = rr & 127;
+        pieces = pieces_of(x.per, x.more, x.item_units, x.snap, (gi * x.nrb + (rr >> 7)) * x.units, x.tiles, c_first);
+    }
+    auto part = [&](int k) {
+        if (pieces == 1)
+            return RowsRef{x.part + (size_t)row * kHeadDim, x.part + (size_t)x.nrows * kHeadDim + row,
+                           x.part + (size_t)x.nrows * (kHeadDim + 1) + row};
+        const float* sl = x.slots + ((size_t)(c_first + k) * 2 + (k == 0)) * x.slot_floats;
+        return RowsRef{sl + in_block * kHeadDim, sl + 128 * kHeadDim + in_block, sl + 128 * (kHeadDim + 1) + in_block};
+    };
     float mm = m;
-    for (int k = 0; k < p.parts; ++k) mm = fmaxf(mm, __ldcg(part_m(p, k, row)));
+#pragma unroll 8
+    for (int k = 0; k < pieces; ++k) mm = fmaxf(mm, __ldcg(part(k).m));
     const float f = weight(m, mm);
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
     l *= f;
-#pragma unroll 4
-    for (int k = 0; k < p.parts; ++k) {
-        const float* pm = part_m(p, k, row);
-        const float fk = weight(__ldcg(pm), mm);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o(p, k, row) + c));
+#pragma unroll 8
+    for (int k = 0; k < pieces; ++k) {
+        const RowsRef r = part(k);
+        const float fk = weight(__ldcg(r.m), mm);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(r.o + c));
         o = make_float4(o.x + fk * v.x, o.y + fk * v.y, o.z + fk * v.z, o.w + fk * v.w);
-        l += fk * __ldcg(pm + part_rows(p) * p.parts);
+        l += fk * __ldcg(r.l);
     }
     m = mm;
 }
@@ -192,6 +225,132 @@ __device__ __forceinline__ void store_row(const PagedParams& p, const RowInfo& x
         make_uint2(tc::pack_bf16x2(o.x * s, o.y * s), tc::pack_bf16x2(o.z * s, o.w * s));
     if (c == 0) p.lse[x.out] = some ? m + __logf(l) : kNegInf;
 }
+// A row that has all its keys (four columns from c): with PREFIX the part that the
+// batch's own keys are joined to, else the output.
+template <bool PREFIX>
+__device__ __forceinline__ void finish_row(const PagedParams& p, const RowInfo& x, int c, float4 o, float m, float l) {
+    if (x.out < 0) return;
+    if (PREFIX) {
+        float* part = p.prefix.part;
+        *reinterpret_cast<float4*>(part + (size_t)x.part * kHeadDim + c) = o;
+        if (c == 0) {
+            part[(size_t)p.prefix.nrows * kHeadDim + x.part] = m;
+            part[(size_t)p.prefix.nrows * (kHeadDim + 1) + x.part] = l;
+        }
+    } else {
+        if (p.prefix.part) join_prefix(p, x.part, c, o, m, l);
+        store_row(p, x, c, o, m, l);
+    }
+}
+
+// ---------------------------------------------------------------- the axis of tiles
+// Items (sequence b, K/V head, row block) one after the other, each kItem units
+// that stand for no tile (its own cost) and one per tile; every CTA takes an equal
+// stretch, moved to an item's end where it would end within kSnap units of one.
+// A: tile sizes (keys) of K/V heads with and without keys, and these constants.
+struct Stretch {
+    int b, gi, rb, len, n;  // item; its keys and tiles (one without keys still takes one, empty, tile: its rows are written)
+    bool keyed;
+    int t0, t1;             // this CTA's tiles of it
+    int pieces, c_first;    // CTAs that share it, and the first of them
+};
+template <class A, bool PREFIX>
+struct AxisWalk {
+    const PagedParams& p;
+    int total, ctas, per, more;  // units; stretch c begins at c * per + min(c, more)
+    int u, end, b, base, len;    // next unit, end of the stretch, current sequence and its first unit
+    __device__ __forceinline__ static int tiles_of(int len, bool keyed) {
+        const int tk = keyed ? A::kTile : A::kTileKeyless;
+        return max(1, (len + tk - 1) / tk);
+    }
+    __device__ __forceinline__ int seq_units(int n) const {
+        return p.nrb * (p.keyed * (tiles_of(n, true) + A::kItem) + (p.Hkv - p.keyed) * (tiles_of(n, false) + A::kItem));
+    }
+    // The item that unit u of a sequence is in; returns its first unit.
+    __device__ __forceinline__ int item_at(int base_u, int n_keys, int unit, Stretch& x) const {
+        int off = unit - base_u;
+        x.n = tiles_of(n_keys, true);
+        const int keyed_units = p.keyed * p.nrb * (x.n + A::kItem);
+        x.keyed = off < keyed_units;
+        int first = 0;
+        if (!x.keyed) {
+            x.n = tiles_of(n_keys, false);
+            off -= keyed_units;
+            first = p.keyed;
+        }
+        const int block = (int)((unsigned)off / (unsigned)(x.n + A::kItem));
+        x.gi = p.by_nrb.div(block);
+        x.rb = block - x.gi * p.nrb;
+        x.gi += first;
+        return unit - (off - block * (x.n + A::kItem));
+    }
+    // By a whole warp: lengths are summed a run of sequences per lane.
+    __device__ __forceinline__ AxisWalk(const PagedParams& params, int cta, int grid) : p(params) {
+        const int lane = threadIdx.x & 31;
+        const int chunk = (p.nseq + 31) >> 5, b_lo = min(lane * chunk, p.nseq), b_hi = min(b_lo + chunk, p.nseq);
+        int mine = 0;
+#pragma unroll 4
+        for (int k = b_lo; k < b_hi; ++k) mine += seq_units(key_len<PREFIX>(p, k));
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += v;
+        }
+        total = __shfl_sync(~0u, incl, 31);
+        const int before = incl - mine;
+        ctas = max(1, min(grid, total / A::kMinUnits));
+        per = (int)((unsigned)total / (unsigned)ctas);
+        more = total - per * ctas;
+        const int lo = cta < ctas ? cta * per + min(cta, more) : total, hi = lo + per + (cta < more ? 1 : 0);
+        // The sequence of a unit below `total`, and its first unit.
+        auto find = [&](int unit, int& seq, int& first) {
+            const int src = __ffs(__ballot_sync(~0u, unit >= before && unit < before + mine)) - 1;
+            int at = before, k = b_lo;
+            if (lane == src)
+                for (;; ++k) {
+                    const int n = seq_units(key_len<PREFIX>(p, k));
+                    if (unit < at + n) break;
+                    at += n;
+                }
+            seq = __shfl_sync(~0u, k, src);
+            first = __shfl_sync(~0u, at, src);
+        };
+        auto snapped = [&](int unit, int seq, int first) {
+            Stretch x;
+            const int start = item_at(first, key_len<PREFIX>(p, seq), unit, x), stop = start + A::kItem + x.n;
+            return unit - start <= A::kItem + A::kSnap ? start : stop - unit <= A::kSnap ? stop : unit;
+        };
+        b = base = 0;
+        u = end = total;
+        if (lo < total) {
+            find(lo, b, base);
+            u = snapped(lo, b, base);
+            if (hi < total) {
+                int b_end, base_end;
+                find(hi, b_end, base_end);
+                end = snapped(hi, b_end, base_end);
+            }
+        }
+        len = key_len<PREFIX>(p, b);
+    }
+    // The next item of the stretch; false: none left.
+    __device__ __forceinline__ bool next(Stretch& x) {
+        if (u >= end) return false;
+        while (u >= base + seq_units(len)) {
+            base += seq_units(len);
+            len = key_len<PREFIX>(p, ++b);
+        }
+        const int start = item_at(base, len, u, x);
+        x.b = b;
+        x.len = len;
+        x.t0 = max(0, u - start - A::kItem);
+        x.t1 = min(x.n, end - start - A::kItem);
+        x.pieces = pieces_of(per, more, A::kItem, A::kSnap, start, x.n, x.c_first);
+        u = start + A::kItem + x.t1;
+        return true;
+    }
+};
 
 // ------------------------------------------------------------------ host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -225,12 +384,16 @@ inline bool make_tmap_pages(const saf_paged_kv& kv, bool keys, int max_rows, CUt
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tensor-core kernel (saf_paged_tc.cu): items of up to 128 rows, the keys of each in p.splits stretches.  With
-// prefix, the stretches become p.parts = p.splits parts; else they are joined, through `slots` and `counters` where
-// there are several.
-constexpr int kTcCtas = 592;  // the most CTAs that stretches make: two waves of two on each of 148 SMs
-inline int tc_items(int nseq, int H_kv, int rows) { return nseq * H_kv * ((rows + 127) / 128); }
-int tc_splits(int items, int max_keys);
+// Units of the longest possible axis must fit 31 bits.
+template <class A>
+bool axis_fits(const PagedParams& p) {
+    const double most = A::kItem + std::max(1, (std::max(p.max_len, p.prefix_len) + A::kTile - 1) / A::kTile);
+    return most * p.nrb * p.Hkv * p.nseq < 2147483648.0;
+}
+// CTAs of either kernel, two per SM; bounds the workspace (pieces: two per CTA).
+constexpr int kMaxGrid = 320;
+inline int paged_grid() { return std::min(kMaxGrid, 2 * sm_count()); }
+// The tensor-core kernel (saf_paged_tc.cu): items of up to 128 rows.
 cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, bool overlap, cudaStream_t stream);
 
 size_t paged_workspace_bytes(int B, int H, int H_kv, int T, int prefix_len);

@@ -1,12 +1,15 @@
 // Attention of many rows over the paged key/value cache on the 5th-generation
 // tensor cores: prompt chunks, and a shared prefix seen by a whole batch.
 //
-// A CTA takes 128 rows of one K/V head (its query heads times the new tokens, and
-// with a shared prefix times the sequences) and one stretch of their keys, in
-// blocks of 128, last block first (patterns tend to favour near keys: the running
-// maximum then starts near where it ends).  Two CTAs per SM, six warps each:
-//   warp 0      producer: page look-up and TMA loads, a box per page, two stages each
-//               of K and V (no K for a K/V head whose query heads are all replaced)
+// An item is 128 rows of one K/V head (its query heads times the new tokens, and
+// with a shared prefix times the sequences), its keys in blocks of 128, last block
+// first (patterns tend to favour near keys: the running maximum then starts near
+// where it ends).  The blocks of all items form one axis, of which every CTA of two
+// per SM takes an equal stretch, as in the kernel for few rows (saf_paged.cu).  An
+// item that several share is joined by the CTA that finishes its last piece, in
+// key order, or with a prefix by those who want its rows.  Six warps:
+//   warp 0      producer: walks the stretch, page look-up and TMA loads, a box per
+//               page, two stages each of K and V (no K where all rows are replaced)
 //   warp 1      TMEM owner and MMA issuer (one elected lane):
 //               S = Q K^T  (tcgen05 SS, 128x128x64), O += P V  (TS, 128x64x128)
 //   warps 2..5  one row per thread: its queries to shared memory, then per block the
@@ -22,10 +25,6 @@
 //                  every thread takes its row from there
 // Rows come head by head, a group's ordinary heads first, so that most warps hold
 // one kind, and blocks of replaced rows alone need no K.
-// With a prefix each stretch is a part that the batch's own keys are joined to;
-// otherwise a row of one stretch is written at once, and of several by the CTA that
-// finishes the row block's last one, in key order.
-//
 // Per block and row: 128 exponentials against 2 x 128 x 64 multiply-adds, so the exp
 // unit (16 a cycle and SM: 2048 cycles for the two CTAs' blocks) bounds it before
 // the tensor pipe (about 770 cycles a block).
@@ -59,9 +58,19 @@ static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4 && PAT_BYTES >= 2 * NEAR_BUF * 4, 
 constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;   // [4 warps] staging area
 constexpr uint32_t SM_ROW = SM_PAT + 4 * PAT_BYTES;  // [128] {head, r at local key 0 within the head's} of a row
 constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
-// TMEM address, last flag, [2] boxes without a page, [4] largest vis of a row warp, [4] whether it has an ordinary row
-constexpr uint32_t SM_MISC = SM_BAR + 16 * 8;
-constexpr uint32_t SM_TOTAL = SM_MISC + 64;
+constexpr uint32_t SM_ITEM = SM_BAR + 20 * 8;  // [2] TcPiece
+constexpr uint32_t SM_MISC = SM_ITEM + 2 * 48;  // TMEM address, last flag, [4] boxes of a K load without a page, [4] of a V load
+constexpr uint32_t SM_TOTAL = SM_MISC + 40;
+
+struct TcAxis {
+    static constexpr int kTile = BN, kTileKeyless = BN, kItem = 2, kSnap = 2, kMinUnits = 8;
+};
+// An item's stretch as the other warps need it: nt blocks from t0 (those that some
+// row sees), keyed: some row is ordinary.
+struct TcPiece {
+    int b, gi, rb, len, t0, nt, keyed, pieces, c_first;  // nt < 0: no more
+};
+static_assert(sizeof(TcPiece) <= 48, "item slot");
 
 // Row max of 128 raw scores: three-input max, four independent chains.
 __device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
@@ -318,31 +327,26 @@ template <bool PREFIX>
 __global__ void __launch_bounds__(NTHREADS, 2)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ PagedParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t bar_kf = sbase + SM_BAR, bar_ke = bar_kf + 8 * NST;  // [NST] K stage full, free (S MMA done)
+    const uint32_t bar_kf = sbase + SM_BAR, bar_ke = bar_kf + 8 * NST;    // [NST] K stage full, free (S MMA done)
     const uint32_t bar_vf = bar_ke + 8 * NST, bar_ve = bar_vf + 8 * NST;  // [NST] V stage full, free (P V MMA done)
-    const uint32_t bar_s = bar_ve + 8 * NST;                            // S ready
+    const uint32_t bar_item = bar_ve + 8 * NST, bar_taken = bar_item + 16;  // [2] item slot full, free (MMA and row warps)
+    const uint32_t bar_q = bar_taken + 16;                              // queries in place (4 warp arrivals)
+    const uint32_t bar_s = bar_q + 8;                                   // S ready
     const uint32_t bar_sf = bar_s + 8;                                  // S copied out by the rows (4 warp arrivals)
     const uint32_t bar_p = bar_sf + 8;                                  // P written (4 warp arrivals)
     const uint32_t bar_o = bar_p + 8;                                   // P V done
+    const uint32_t bar_join = bar_o + 8;                                // row warps together (4 warp arrivals)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SM_MISC);
     volatile int* last_flag = reinterpret_cast<int*>(smem + SM_MISC + 4);
-    volatile uint32_t* meta = reinterpret_cast<uint32_t*>(smem + SM_MISC + 8);
-    int *warp_vis = reinterpret_cast<int*>(smem + SM_MISC + 16), *warp_keyed = warp_vis + 4;
+    volatile uint32_t *kmeta = reinterpret_cast<uint32_t*>(smem + SM_MISC + 8), *vmeta = kmeta + 4;
+    TcPiece* items = reinterpret_cast<TcPiece*>(smem + SM_ITEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    // row block (neighbouring CTAs share their keys), stretch, K/V head, sequence
-    int id = blockIdx.x;
-    const int rb = id % p.nrb;
-    id /= p.nrb;
-    const int split = id % p.splits;
-    id /= p.splits;
-    const int gi = id % p.Hkv, b = id / p.Hkv;
-    const int g = p.order[gi];
-    const int len = key_len<PREFIX>(p, b), n_all = (len + BN - 1) / BN;
-    const int t0 = (int)((long long)split * n_all / p.splits), t_end = (int)((long long)(split + 1) * n_all / p.splits);
+    if (sbase & 1023u) {  // the swizzled tiles need what the declaration asks for
+        if (threadIdx.x == 0) report(p.err, 0x504);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -350,11 +354,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             mbar_init(bar_ke + 8 * s, 1);
             mbar_init(bar_vf + 8 * s, 1);
             mbar_init(bar_ve + 8 * s, 1);
+            mbar_init(bar_item + 8 * s, 1);
+            mbar_init(bar_taken + 8 * s, 5);
         }
+        mbar_init(bar_q, 4);
         mbar_init(bar_s, 1);
         mbar_init(bar_sf, 4);
         mbar_init(bar_p, 4);
         mbar_init(bar_o, 1);
+        mbar_init(bar_join, 4);
         fence_mbar_init();
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -364,320 +372,409 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         tmem_relinquish();
     }
     if (PREFIX) griddep_launch_dependents();  // the batch's own keys may start
-
-    // ---- the rows
-    const int quarter = warp & 3, row = quarter * 32 + lane;  // (row threads)
-    RowInfo info;
-    info.out = -1;
-    info.vis = info.replaced = 0;
-    if (warp >= 2) {
-        const int n = PREFIX ? 0 : new_tokens(p, b);
-        info = row_info<PREFIX>(p, b, g, len, n, p.prefix_len + len - n, rb * BM + row);
-        const int most = __reduce_max_sync(~0u, info.vis);
-        const int ordinary = __any_sync(~0u, info.out >= 0 && !info.replaced);
-        if (lane == 0) {
-            warp_vis[quarter] = most;
-            warp_keyed[quarter] = ordinary;
-        }
-        const int head = max(info.replaced - 1, 0);
-        reinterpret_cast<int2*>(smem + SM_ROW)[row] = make_int2(head, (int)(info.r0 - (long long)head * p.pattern_len));
-        if (gi < p.keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(info.out, 0) * kHeadDim);
-            const bool read = info.out >= 0 && !info.replaced;
-            uint4 w[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) w[c] = read ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                st_shared_v4(sbase + SM_Q + row * 128 + ((c ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
-            fence_proxy_async_smem();
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // blocks that some row sees
-    const int most = max(max(warp_vis[0], warp_vis[1]), max(warp_vis[2], warp_vis[3]));
-    const int nt = max(0, min(t_end, (most + BN - 1) / BN) - t0);
-    const bool keyed = warp_keyed[0] | warp_keyed[1] | warp_keyed[2] | warp_keyed[3];  // the block reads K
 
     if (warp == 0) {
         // ------------------------------------------------ producer
         const int lp = p.log_page, lb = min(lp, 7);  // page and box rows
         const uint32_t box_bytes = 128u << lb;
         const int boxes = BN >> lb;
-        const int32_t* table = p.table + (size_t)b * p.table_stride;
+        AxisWalk<TcAxis, PREFIX> walk(p, blockIdx.x, gridDim.x);
+        int nk = 0, nv = 0;  // K and V loads so far
         bool ok = true;
-        int page = -1, loaded = -1;  // this lane's box of block `loaded`
-        bool need = false;
-        auto look_up = [&](int i) {
-            if (loaded == i) return;
-            loaded = i;
-            const int key = (t0 + nt - 1 - i) * BN + (lane << lb);
-            need = lane < boxes && key < len;
-            page = need ? __ldg(table + (key >> lp)) : -1;
-        };
-        auto load = [&](int i, bool keys) {
-            look_up(i);
-            const int s = i & 1;
-            const uint32_t full = (keys ? bar_kf : bar_vf) + 8 * s, empty = (keys ? bar_ke : bar_ve) + 8 * s;
-            const bool good = need && page >= 0 && page < p.num_pages;
-            const uint32_t bad = __ballot_sync(~0u, lane < boxes && !good);
-            const int loads = __popc(__ballot_sync(~0u, good));
-            if (!mbar_wait_warp(empty, ((i >> 1) & 1) ^ 1, kWaitLimit)) return false;
-            if (lane == 0) {
-                if (!keys) meta[s] = bad;
-                mbar_expect_tx(full, loads * box_bytes);
+        for (int ni = 0; ok; ++ni) {
+            Stretch w;
+            TcPiece x;
+            x.nt = -1;
+            if (walk.next(w)) {
+                x.b = w.b;
+                x.gi = w.gi;
+                x.rb = w.rb;
+                x.len = w.len;
+                x.t0 = w.t0;
+                x.pieces = w.pieces;
+                x.c_first = w.c_first;
+                const int n = PREFIX ? 0 : new_tokens(p, w.b);
+                int most = 0, ordinary = 0;
+#pragma unroll 1
+                for (int r = lane; r < BM; r += 32) {
+                    const RowInfo row = row_info<PREFIX>(p, w.b, w.gi, w.len, n, p.prefix_len + w.len - n, w.rb * BM + r);
+                    most = max(most, row.vis);
+                    ordinary |= row.out >= 0 && !row.replaced;
+                }
+                most = __reduce_max_sync(~0u, most);
+                x.keyed = __any_sync(~0u, ordinary);
+                x.nt = max(0, min(w.t1, (most + BN - 1) / BN) - w.t0);
             }
-            __syncwarp();
-            if (good)
-                tma_load_4d(sbase + (keys ? SM_K : SM_V) + s * TILE_BYTES + lane * box_bytes, keys ? &tmK : &tmV, full, 0,
-                            ((t0 + nt - 1 - i) * BN + (lane << lb)) & ((1 << lp) - 1), g, page);
-            return true;
-        };
-        // K runs a block ahead of V, as S runs ahead of P V
-        int issued_k = 0, issued_v = 0;
-        for (int i = 0; ok && i < nt; ++i) {
-            if (keyed && i == 0) ok = load(0, true), issued_k = 1;
-            if (ok) ok = load(i, false), issued_v = i + 1;
-            if (ok && keyed && i + 1 < nt) ok = load(i + 1, true), issued_k = i + 2;
+            const int slot = ni & 1;
+            ok = mbar_wait_warp(bar_taken + 8 * slot, ((ni >> 1) & 1) ^ 1, kWaitLimit);
+            if (!ok) break;
+            if (lane == 0) {
+                items[slot] = x;
+                mbar_arrive(bar_item + 8 * slot);
+            }
+            if (x.nt < 0) break;
+            const int32_t* table = p.table + (size_t)x.b * p.table_stride;
+            const int g = p.order[w.gi];
+            // pages of this lane's boxes of the last two blocks looked up (block i in entry i & 1)
+            int pages[2] = {-1, -1}, looked = 0;
+            auto load = [&](int i, bool keys) {
+                const int key = (x.t0 + x.nt - 1 - i) * BN + (lane << lb);
+                const bool need = lane < boxes && key < x.len;
+                if (i >= looked) {
+                    const int page = need ? __ldg(table + (key >> lp)) : -1;
+                    if (i & 1) pages[1] = page;
+                    else pages[0] = page;
+                    looked = i + 1;
+                }
+                const int page = (i & 1) ? pages[1] : pages[0];
+                const int at = keys ? nk++ : nv++, s = at & 1;
+                const uint32_t full = (keys ? bar_kf : bar_vf) + 8 * s, empty = (keys ? bar_ke : bar_ve) + 8 * s;
+                const bool good = need && page >= 0 && page < p.num_pages;
+                const uint32_t bad = __ballot_sync(~0u, lane < boxes && !good);
+                const int loads = __popc(__ballot_sync(~0u, good));
+                if (!mbar_wait_warp(empty, ((at >> 1) & 1) ^ 1, kWaitLimit)) {
+                    --(keys ? nk : nv);
+                    return false;
+                }
+                if (lane == 0) {
+                    // four entries: the rows may still be two loads behind the stage that is being filled
+                    (keys ? kmeta : vmeta)[at & 3] = bad;
+                    mbar_expect_tx(full, loads * box_bytes);
+                }
+                __syncwarp();
+                if (good)
+                    tma_load_4d(sbase + (keys ? SM_K : SM_V) + s * TILE_BYTES + lane * box_bytes, keys ? &tmK : &tmV, full, 0,
+                                key & ((1 << lp) - 1), g, page);
+                return true;
+            };
+            // K_{i+1} before V_i, whose stage frees later: S runs ahead of P V
+            if (x.keyed && x.nt > 0) ok = load(0, true);
+            for (int i = 0; ok && i < x.nt; ++i) {
+                if (x.keyed && i + 1 < x.nt) ok = load(i + 1, true);
+                if (ok) ok = load(i, false);
+            }
         }
         if (!ok && lane == 0) {  // a wait gave up: the loads in flight land (or give up in turn) before the memory is let go
             report(p.err, 0x501);
-            for (int i = max(0, issued_k - 2); i < issued_k - 1; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
-            for (int i = max(0, issued_v - 2); i < issued_v - 1; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+            for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+            for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (see fwd_tc for the elected lane)
+        // ------------------------------------------------ MMA issuer (one elected lane, as in the layer's kernels)
         const uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q (K-major) x K (K-major)
         const uint32_t idO = idesc_bf16(128, 64, 0, 1);   // P (TMEM) x V (MN-major)
         constexpr uint64_t kStage = TILE_BYTES >> 4;
         const uint64_t dQ = sw128_desc(sbase + SM_Q), dK0 = sw128_desc(sbase + SM_K), dV0 = sw128_desc(sbase + SM_V);
+        int nk = 0, nv = 0, nq = 0;  // S and P V products issued, items with queries
         bool ok = true;
-        auto issue_s = [&](int i) {
-            const int s = i & 1;
-            if (!mbar_wait_warp(bar_kf + 8 * s, (i >> 1) & 1, kWaitLimit)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss(tmem, dQ + 2 * k, dK0 + s * kStage + 2 * k, idS, k > 0 ? 1u : 0u);
-                mma_commit(bar_s);
-                mma_commit(bar_ke + 8 * s);
-            }
-            __syncwarp();
-            return true;
-        };
-        if (keyed && nt > 0) ok = issue_s(0);
-        for (int i = 0; ok && i < nt; ++i) {
-            if (keyed && i + 1 < nt) ok = mbar_wait_warp(bar_sf, i & 1, kWaitLimit) && issue_s(i + 1);
-            const int s = i & 1;
-            ok = ok && mbar_wait_warp(bar_vf + 8 * s, (i >> 1) & 1, kWaitLimit) && mbar_wait_warp(bar_p, i & 1, kWaitLimit);
+        for (int ni = 0; ok; ++ni) {
+            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
             if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(tmem + TO_COL, tmem + TP_COL + 8 * k, dV0 + s * kStage + 128 * k, idO, (i > 0 || k > 0) ? 1u : 0u);
-                mma_commit(bar_o);
-                mma_commit(bar_ve + 8 * s);
-            }
+            const int nt = items[ni & 1].nt;
+            const bool keyed = items[ni & 1].keyed && nt > 0;
             __syncwarp();
+            if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
+            if (nt < 0) break;
+            auto issue_s = [&] {
+                const int s = nk & 1;
+                // the rows have copied the S before (an item's first: that item's last)
+                if (nk > 0 && !mbar_wait_warp(bar_sf, (nk - 1) & 1, kWaitLimit)) return false;
+                if (!mbar_wait_warp(bar_kf + 8 * s, (nk >> 1) & 1, kWaitLimit)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmem, dQ + 2 * k, dK0 + s * kStage + 2 * k, idS, k > 0 ? 1u : 0u);
+                    mma_commit(bar_s);
+                    mma_commit(bar_ke + 8 * s);
+                }
+                __syncwarp();
+                ++nk;
+                return true;
+            };
+            if (keyed) {
+                ok = mbar_wait_warp(bar_q, nq & 1, kWaitLimit) && issue_s();
+                ++nq;
+            }
+            for (int i = 0; ok && i < nt; ++i) {
+                if (keyed && i + 1 < nt) ok = issue_s();
+                const int s = nv & 1;
+                ok = ok && mbar_wait_warp(bar_vf + 8 * s, (nv >> 1) & 1, kWaitLimit) && mbar_wait_warp(bar_p, nv & 1, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tmem + TO_COL, tmem + TP_COL + 8 * k, dV0 + s * kStage + 128 * k, idO, (i > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(bar_o);
+                    mma_commit(bar_ve + 8 * s);
+                }
+                __syncwarp();
+                ++nv;
+            }
         }
         if (!ok && lane == 0) report(p.err, 0x502);
     } else {
         // ------------------------------------------------ row threads
+        const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + TO_COL, tP = tmem + lane_off + TP_COL;
         const int lb = min(p.log_page, 7);
-        const bool rep = info.out >= 0 && info.replaced;
-        const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : INT_MAX);
-        const float unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
-        Patterns pt;
-        pt.reps = __ballot_sync(~0u, rep && info.vis > 0);
-        const bool looks = (pt.reps >> lane) & 1u;
-        const int from = pt.reps ? __ffs(pt.reps) - 1 : 0;
-        const long long a_first = __shfl_sync(~0u, info.a0, from), r_first = __shfl_sync(~0u, info.r0, from);
-        pt.a = p.a + a_first;
-        pt.r = p.r + r_first;
-        pt.a0 = p.a + (PREFIX ? 0 : p.prefix_len);
-        pt.r0 = p.r;
-        pt.pattern_len = p.pattern_len;
-        pt.rows = reinterpret_cast<const int2*>(smem + SM_ROW) + quarter * 32;
-        pt.pat = reinterpret_cast<float*>(smem + SM_PAT + quarter * PAT_BYTES);
-        pt.one_head = __all_sync(~0u, !looks || info.a0 == a_first);
-        // all rows with a token look up, by one head's vectors: the others ride along on the first one's
-        const bool pure = pt.reps && pt.one_head && __all_sync(~0u, info.out < 0 || looks);
-        const int off = looks && pt.one_head ? (int)(info.r0 - r_first) : 0;  // (within a head's vector)
-        const int low = __reduce_min_sync(~0u, off);
-        pt.span = __reduce_max_sync(~0u, off) - low;
-        const bool near = pt.span <= NEAR_SPAN;
-        FarRows far;
-        bool primed = false;
-        if (pure && !near) {
-            // the stretch of the 16 keys from key k on begins 15 floats before r's entry of key k
-            const long long start = r_first + off - 15;
-            const int edge = (int)((start & ~3ll) - r_first);
-            far.shift = (int)(start & 3);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) far.src[i] = __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3);
-            far.src[4] = edge + 16;
-            far.room = (long long)p.H * p.pattern_len - (r_first + edge + 16);
-        }
-        float m = kNegInf, l = 0.f;  // running maximum (in the row's units), sum
-        bool ok = true;
-        for (int i = 0; i < nt; ++i) {
-            const int k0 = (t0 + nt - 1 - i) * BN;
-            // V has landed: its pages are known
-            ok = mbar_wait_warp(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
-            if (ok && keyed) ok = mbar_wait_warp(bar_s, i & 1, kWaitLimit);
+        int nk = 0, nv = 0, joins = 0;  // S and P V products, joins of the row warps so far
+        bool ok = true, waited = false;
+        // A barrier of the row warps, bounded like every wait.
+        auto join_warps = [&] {
+            mbar_arrive_warp(bar_join);
+            if (ok) ok = mbar_wait_warp(bar_join, joins & 1, kWaitLimit);
+            ++joins;
+        };
+        for (int ni = 0; ok; ++ni) {
+            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t bad = meta[i & 1];
-            if (pt.reps || k0 + BN > vmin || bad) {
-                if (i > 0) {  // P V of the block before has read P and added to O
-                    ok = mbar_wait_warp(bar_o, (i - 1) & 1, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                float2 ml;
-                if (pure && k0 + BN <= vmin && !bad) {
-                    const bool next = i + 1 < nt;
-                    ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off - low, tO, tP, k0)
-                              : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
-                    primed = next;
-                } else {
-                    if (primed) {  // copies begun for this block: its staging area is wanted
-                        asm volatile("cp.async.wait_all;\n" ::: "memory");
-                        __syncwarp();
-                        primed = false;
-                    }
-                    ml = mixed_block(m, l, pt, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, len, bad, lb);
-                }
-                m = ml.x;
-                l = ml.y;
-                if (keyed) {
-                    tc_fence_before();
-                    mbar_arrive_warp(bar_sf);
-                }
-            } else {
-                uint32_t v[128];
+            const TcPiece x = items[ni & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
+            if (x.nt < 0) break;
+            const int n_new = PREFIX ? 0 : new_tokens(p, x.b);
+            const RowInfo info = row_info<PREFIX>(p, x.b, x.gi, x.len, n_new, p.prefix_len + x.len - n_new, x.rb * BM + row);
+            const bool keyed = x.keyed && x.nt > 0;
+            if (keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(info.out, 0) * kHeadDim);
+                const bool read = info.out >= 0 && !info.replaced;
+                uint4 w[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-                tmem_wait_ld();
-                tc_fence_before();
-                mbar_arrive_warp(bar_sf);  // the MMA warp may now overwrite S
-                const float mx = row_max(v);
-                float f = 1.f;
-                if ((mx - m) * unit > 8.f) {
-                    f = ex2((m - mx) * unit);
-                    l *= f;
-                    m = mx;
-                }
-                if (i > 0) {
-                    ok = mbar_wait_warp(bar_o, (i - 1) & 1, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                const float nm = m == kNegInf ? 0.f : -m * unit;
-                const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
-                uint64_t l2[4] = {0, 0, 0, 0};
-                exp_quarter<0>(v, unit2, nm2, l2, tP);
-                exp_quarter<1>(v, unit2, nm2, l2, tP);
-                exp_quarter<2>(v, unit2, nm2, l2, tP);
-                exp_quarter<3>(v, unit2, nm2, l2, tP);
-                const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
-                l += s2.x + s2.y;
-                if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
-            }
-            if (k0 + BN > len || bad) {
-                // slots without a token may hold a NaN, and 0 times that is one: their V rows become zeros
-                if (k0 + row >= len || ((bad >> (row >> lb)) & 1u)) {
+                for (int c = 0; c < 8; ++c) w[c] = read ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) st_shared_v4(sbase + SM_V + (i & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
-                }
+                for (int c = 0; c < 8; ++c)
+                    st_shared_v4(sbase + SM_Q + row * 128 + ((c ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
                 fence_proxy_async_smem();
+                mbar_arrive_warp(bar_q);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive_warp(bar_p);
-        }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-        if (ok && nt > 0) ok = mbar_wait_warp(bar_o, (nt - 1) & 1, kWaitLimit);
-        if (!ok && lane == 0) report(p.err, 0x503);
-        tc_fence_after();
-        if (!rep) m *= 0.125f;
-        if (!PREFIX && p.part) griddep_wait();
-        // ---- the rows out: a part of the prefix, a piece of several, or the output
-        const bool pieces = !PREFIX && p.splits > 1;
-        const size_t item = ((size_t)b * p.Hkv + gi) * p.nrb + rb;
-        float* slot = p.slots + (item * p.splits + split) * BM * (kHeadDim + 2);
-        float mo = m, lo = l;
+            const bool rep = info.out >= 0 && info.replaced;
+            const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : INT_MAX);
+            const uint32_t reps = __ballot_sync(~0u, rep && info.vis > 0);
+            const float unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
+            float m = kNegInf, l = 0.f;  // running maximum (in the row's units), sum
+            // Block i has landed, with its scores where it has some; boxes without a page in `bad`.
+            auto arrived = [&](int i, uint32_t& bad) {
+                if (keyed) {
+                    // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load
+                    // was seen by the MMA warp before it issued S)
+                    ok = mbar_wait_warp(bar_s, nk & 1, kWaitLimit);
+                    bad = kmeta[nk & 3];
+                    ++nk;
+                } else {
+                    ok = mbar_wait_warp(bar_vf + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+                    bad = vmeta[nv & 3];
+                }
+                tc_fence_after();
+                return ok;
+            };
+            // P V of the block before has read P and added to O.
+            auto p_free = [&](int i) {
+                if (i == 0) return true;
+                ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
+                tc_fence_after();
+                return ok;
+            };
+            // P of the block is in place.  Slots without a token may hold a NaN, and 0 times that is one: their V rows
+            // become zeros first.
+            auto hand_over = [&](int k0, uint32_t bad) {
+                if (k0 + BN > x.len || bad) {
+                    ok = mbar_wait_warp(bar_vf + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+                    if (k0 + row >= x.len || ((bad >> (row >> lb)) & 1u)) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t ov[32];
-            if (nt > 0) {
-                tmem_ld32(tO + 32 * c, ov);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] = 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float4 o = make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                                       __uint_as_float(ov[e + 3]));
-                const int col = 32 * c + e;
-                if (pieces) {
-                    __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + col), o);
-                } else if (info.out >= 0) {
-                    if (PREFIX) {
-                        *reinterpret_cast<float4*>(part_o(p, split, info.part) + col) = o;
+                        for (int c = 0; c < 8; ++c)
+                            st_shared_v4(sbase + SM_V + (nv & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive_warp(bar_p);
+                ++nv;
+                return ok;
+            };
+            if (!reps) {
+                for (int i = 0; i < x.nt; ++i) {
+                    const int k0 = (x.t0 + x.nt - 1 - i) * BN;
+                    uint32_t bad;
+                    if (!arrived(i, bad)) break;
+                    if (k0 + BN > vmin || bad) {
+                        if (!p_free(i)) break;
+                        const float2 ml = mixed_block(m, l, Patterns{}, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, x.len, bad, lb);
+                        m = ml.x;
+                        l = ml.y;
+                        if (keyed) {
+                            tc_fence_before();
+                            mbar_arrive_warp(bar_sf);
+                        }
                     } else {
-                        mo = m;
-                        lo = l;
-                        if (p.part) join_parts(p, info.part, col, o, mo, lo);
-                        store_row(p, info, col, o, mo, lo);
+                        uint32_t v[128];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        if (keyed) mbar_arrive_warp(bar_sf);  // the MMA warp may now overwrite S
+                        const float mx = row_max(v);
+                        float f = 1.f;
+                        if ((mx - m) * unit > 8.f) {
+                            f = ex2((m - mx) * unit);
+                            l *= f;
+                            m = mx;
+                        }
+                        if (!p_free(i)) break;
+                        const float nm = m == kNegInf ? 0.f : -m * unit;
+                        const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
+                        uint64_t l2[4] = {0, 0, 0, 0};
+                        exp_quarter<0>(v, unit2, nm2, l2, tP);
+                        exp_quarter<1>(v, unit2, nm2, l2, tP);
+                        exp_quarter<2>(v, unit2, nm2, l2, tP);
+                        exp_quarter<3>(v, unit2, nm2, l2, tP);
+                        const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
+                        l += s2.x + s2.y;
+                        if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
                     }
+                    if (!hand_over(k0, bad)) break;
+                }
+            } else {
+                const int head = max(info.replaced - 1, 0);
+                const bool looks = (reps >> lane) & 1u;
+                const int from = __ffs(reps) - 1;
+                const long long a_first = __shfl_sync(~0u, info.a0, from), r_first = __shfl_sync(~0u, info.r0, from);
+                reinterpret_cast<int2*>(smem + SM_ROW)[row] = make_int2(head, (int)(info.r0 - (long long)head * p.pattern_len));
+                __syncwarp();
+                Patterns pt;
+                pt.reps = reps;
+                pt.a = p.a + a_first;
+                pt.r = p.r + r_first;
+                pt.a0 = p.a + (PREFIX ? 0 : p.prefix_len);
+                pt.r0 = p.r;
+                pt.pattern_len = p.pattern_len;
+                pt.rows = reinterpret_cast<const int2*>(smem + SM_ROW) + quarter * 32;
+                pt.pat = reinterpret_cast<float*>(smem + SM_PAT + quarter * PAT_BYTES);
+                pt.one_head = __all_sync(~0u, !looks || info.a0 == a_first);
+                // all rows with a token look up, by one head's vectors: the others ride along on the first one's
+                const bool pure = pt.one_head && __all_sync(~0u, info.out < 0 || looks);
+                const int off = looks && pt.one_head ? (int)(info.r0 - r_first) : 0;  // (within a head's vector)
+                const int low = __reduce_min_sync(~0u, off);
+                pt.span = __reduce_max_sync(~0u, off) - low;
+                const bool near = pt.span <= NEAR_SPAN;
+                FarRows far;
+                bool primed = false;
+                if (pure && !near) {
+                    // the stretch of the 16 keys from key k on begins 15 floats before r's entry of key k
+                    const long long start = r_first + off - 15;
+                    const int edge = (int)((start & ~3ll) - r_first);
+                    far.shift = (int)(start & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) far.src[i] = __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3);
+                    far.src[4] = edge + 16;
+                    far.room = (long long)p.H * p.pattern_len - (r_first + edge + 16);
+                }
+                for (int i = 0; i < x.nt; ++i) {
+                    const int k0 = (x.t0 + x.nt - 1 - i) * BN;
+                    uint32_t bad;
+                    if (!arrived(i, bad) || !p_free(i)) break;
+                    float2 ml;
+                    if (pure && k0 + BN <= vmin && !bad) {
+                        const bool next = i + 1 < x.nt;
+                        ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off - low, tO, tP, k0)
+                                  : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
+                        primed = next;
+                    } else {
+                        if (primed) {  // copies begun for this block: its staging area is wanted
+                            asm volatile("cp.async.wait_all;\n" ::: "memory");
+                            __syncwarp();
+                            primed = false;
+                        }
+                        ml = mixed_block(m, l, pt, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, x.len, bad, lb);
+                    }
+                    m = ml.x;
+                    l = ml.y;
+                    if (keyed) {
+                        tc_fence_before();
+                        mbar_arrive_warp(bar_sf);
+                    }
+                    if (!hand_over(k0, bad)) break;
+                }
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                __syncwarp();
+            }
+            if (ok && x.nt > 0) ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
+            tc_fence_after();
+            if (!ok) break;
+            if (!rep) m *= 0.125f;
+            if (!PREFIX && p.prefix.part && !waited) {
+                griddep_wait();
+                waited = true;
+            }
+            // ---- the rows out, or a piece of them
+            constexpr int SLOT = BM * (kHeadDim + 2);
+            float* slot = p.slots + ((size_t)blockIdx.x * 2 + (x.t0 == 0)) * SLOT;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t ov[32];
+                if (x.nt > 0) {
+                    tmem_ld32(tO + 32 * c, ov);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 o = make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                                 __uint_as_float(ov[e + 3]));
+                    if (x.pieces > 1) __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + 32 * c + e), o);
+                    else finish_row<PREFIX>(p, info, 32 * c + e, o, m, l);
                 }
             }
-        }
-        if (PREFIX && info.out >= 0) store_part_ml(p, split, info.part, m, l);
-        if (pieces) {
-            __stcg(slot + BM * kHeadDim + row, m);
-            __stcg(slot + BM * (kHeadDim + 1) + row, l);
-            __threadfence();
-            named_sync(1, 128);
-            if (row == 0) *last_flag = atomicAdd(p.counters + item, 1u) == (unsigned)p.splits - 1;
-            named_sync(1, 128);
-            if (*last_flag) {
+            tc_fence_before();  // (O is read before the next item's first P V, which waits for this thread's P)
+            if (x.pieces > 1) {
+                __stcg(slot + BM * kHeadDim + row, m);
+                __stcg(slot + BM * (kHeadDim + 1) + row, l);
+            }
+            if (!PREFIX && x.pieces > 1) {  // (a prefix's pieces are joined where they are wanted)
                 __threadfence();
-                const float* first = p.slots + item * p.splits * BM * (kHeadDim + 2);
-                constexpr int STRIDE = BM * (kHeadDim + 2);
-                const int n = new_tokens(p, b);
-                const int c = (row & 15) * 4;
-                for (int rr = row >> 4; rr < BM; rr += 8) {
-                    const RowInfo x = row_info<false>(p, b, g, len, n, p.prefix_len + len - n, rb * BM + rr);
-                    if (x.out < 0) continue;  // alike in the sixteen threads of a row
-                    float mm = kNegInf;
-                    for (int k = 0; k < p.splits; ++k) mm = fmaxf(mm, __ldcg(first + (size_t)k * STRIDE + BM * kHeadDim + rr));
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float ll = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < p.splits; ++k) {
-                        const float* sl = first + (size_t)k * STRIDE;
-                        const float fk = weight(__ldcg(sl + BM * kHeadDim + rr), mm);
-                        const float4 w = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c));
-                        o = make_float4(o.x + fk * w.x, o.y + fk * w.y, o.z + fk * w.z, o.w + fk * w.w);
-                        ll += fk * __ldcg(sl + BM * (kHeadDim + 1) + rr);
+                join_warps();
+                if (row == 0) *last_flag = atomicAdd(p.counters + x.c_first, 1u) == (unsigned)x.pieces - 1;
+                join_warps();
+                if (ok && *last_flag) {
+                    __threadfence();
+                    auto slot_of = [&](int k) { return p.slots + ((size_t)(x.c_first + k) * 2 + (k == 0)) * SLOT; };
+                    const int c = (row & 3) * 16;  // four threads to a row
+#pragma unroll 1
+                    for (int rr = row >> 2; rr < BM; rr += 32) {
+                        const RowInfo y = row_info<PREFIX>(p, x.b, x.gi, x.len, n_new, p.prefix_len + x.len - n_new, x.rb * BM + rr);
+                        float mm = kNegInf;
+                        for (int k = 0; k < x.pieces; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + BM * kHeadDim + rr));
+                        float4 o[4] = {};
+                        float ll = 0.f;
+#pragma unroll 2
+                        for (int k = 0; k < x.pieces; ++k) {
+                            const float* sl = slot_of(k);
+                            const float fk = weight(__ldcg(sl + BM * kHeadDim + rr), mm);
+                            ll += fk * __ldcg(sl + BM * (kHeadDim + 1) + rr);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c + 4 * q));
+                                o[q] = make_float4(o[q].x + fk * v.x, o[q].y + fk * v.y, o[q].z + fk * v.z, o[q].w + fk * v.w);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) finish_row<PREFIX>(p, y, c + 4 * q, o[q], mm, ll);
                     }
-                    if (p.part) join_parts(p, x.part, c, o, mm, ll);
-                    store_row(p, x, c, o, mm, ll);
+                    if (row == 0) atomicExch(p.counters + x.c_first, 0u);
                 }
-                if (row == 0) atomicExch(p.counters + item, 0u);
+                join_warps();
             }
         }
+        if (!ok && lane == 0) report(p.err, 0x503);
     }
     tc_fence_before();
     __syncthreads();
@@ -694,13 +791,28 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStr
     p.nrb = (p.rows + BM - 1) / BM;
     p.by_T = divisor(p.T);
     p.by_BT = divisor(p.B * p.T);
-    const double ctas = (double)p.nseq * p.Hkv * p.nrb * p.splits;
-    if (ctas >= 2147483648.0) return cudaErrorNotSupported;
-    const int smem = SM_TOTAL + 1024;
+    p.by_nrb = divisor(p.nrb);
+    if (!axis_fits<TcAxis>(p)) return cudaErrorNotSupported;
+    if (PREFIX) {  // for those that join it: AxisWalk's own figures, there being one sequence of known length
+        PrefixParts& x = p.prefix;
+        x.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
+        x.units = x.tiles + TcAxis::kItem;
+        x.item_units = TcAxis::kItem;
+        x.snap = TcAxis::kSnap;
+        x.nrb = p.nrb;
+        x.rows = p.rows;
+        x.by_rows = divisor(p.rows);
+        const int total = p.Hkv * p.nrb * x.units, ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
+        x.per = total / ctas;
+        x.more = total - x.per * ctas;
+        x.slots = p.slots;
+        x.slot_floats = BM * (kHeadDim + 2);
+    }
+    const int smem = SM_TOTAL;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.gridDim = dim3((unsigned)paged_grid());
     cfg.blockDim = dim3(NTHREADS);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
@@ -718,23 +830,6 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStr
 }
 
 }  // namespace
-
-// Stretches of the keys: the fewest waves of CTAs (two per SM) times blocks per
-// CTA, an item's own cost counted as four blocks.
-int tc_splits(int items, int max_keys) {
-    const int tiles = std::max(1, (max_keys + BN - 1) / BN);
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= tiles && (s == 1 || (int64_t)items * s <= kTcCtas); ++s) {
-        const double waves = (double)(((int64_t)items * s + 295) / 296);
-        const double cost = waves * ((tiles + s - 1) / s + 4);
-        if (s == 1 || cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
-}
 
 cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, bool overlap, cudaStream_t stream) {
     return prefix ? launch<true>(kv, p, overlap, stream) : launch<false>(kv, p, overlap, stream);
