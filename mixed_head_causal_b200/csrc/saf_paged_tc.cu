@@ -323,24 +323,178 @@ __device__ __noinline__ float2 mixed_block(float m, float l, const Patterns w, f
     return make_float2(m, l);
 }
 
+// The barriers and per-load words, by the offsets that the kernel lays them out at.
+constexpr uint32_t BAR_KF = SM_BAR, BAR_KE = BAR_KF + 8 * NST;      // [NST] K stage full, free (S MMA done)
+constexpr uint32_t BAR_VF = BAR_KE + 8 * NST, BAR_VE = BAR_VF + 8 * NST;  // [NST] V stage full, free (P V MMA done)
+constexpr uint32_t BAR_ITEM = BAR_VE + 8 * NST, BAR_TAKEN = BAR_ITEM + 16;  // [2] item slot full, free (MMA and row warps)
+constexpr uint32_t BAR_Q = BAR_TAKEN + 16;                          // queries in place (4 warp arrivals)
+constexpr uint32_t BAR_S = BAR_Q + 8;                               // S ready
+constexpr uint32_t BAR_SF = BAR_S + 8;                              // S copied out by the rows (4 warp arrivals)
+constexpr uint32_t BAR_P = BAR_SF + 8;                              // P written (4 warp arrivals)
+constexpr uint32_t BAR_O = BAR_P + 8;                               // P V done
+constexpr uint32_t BAR_JOIN = BAR_O + 8;                            // row warps together (4 warp arrivals)
+static_assert(BAR_JOIN + 8 <= SM_ITEM, "barrier area");
+constexpr uint32_t SM_KMETA = SM_MISC + 8, SM_VMETA = SM_MISC + 24;
+
+// The blocks of an item as a row warp goes through them: nt blocks, the first of
+// which begins at key k_first (they go down from there).  nk, nv: S and P V
+// products before it.  The two loops below are functions of their own so that
+// what an item needs otherwise does not crowd the 128 scores out of the registers
+// (spilled, the loop took twice as long).
+struct RowLoop {
+    uint32_t sbase, tmem;  // tmem: of this warp's lanes
+    int nt, k_first, len, nk, nv, lb, vis, vmin;
+    float unit;
+    bool keyed;
+};
+struct RowResult {
+    float m, l;
+    bool ok;
+};
+// Block i has landed, with its scores where it has some; boxes without a page in `bad`.
+__device__ __forceinline__ bool block_arrived(const RowLoop& w, int i, uint32_t& bad) {
+    bool ok;
+    if (w.keyed) {
+        // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load was
+        // seen by the MMA warp before it issued S)
+        ok = mbar_wait_warp(w.sbase + BAR_S, (w.nk + i) & 1, kWaitLimit);
+        bad = ld_shared_u32(w.sbase + SM_KMETA + 4 * ((w.nk + i) & 3));
+    } else {
+        const int at = w.nv + i;
+        ok = mbar_wait_warp(w.sbase + BAR_VF + 8 * (at & 1), (at >> 1) & 1, kWaitLimit);
+        bad = ld_shared_u32(w.sbase + SM_VMETA + 4 * (at & 3));
+    }
+    tc_fence_after();
+    return ok;
+}
+// P V of the block before has read P and added to O (an item's first: waited for by the item before).
+__device__ __forceinline__ bool p_free(const RowLoop& w, int i) {
+    if (i == 0) return true;
+    const bool ok = mbar_wait_warp(w.sbase + BAR_O, (w.nv + i - 1) & 1, kWaitLimit);
+    tc_fence_after();
+    return ok;
+}
+__device__ __forceinline__ void hand_over(const RowLoop& w) {
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive_warp(w.sbase + BAR_P);
+}
+// Slots without a token may hold a NaN, and 0 times that is one: their V rows become
+// zeros before P V reads them.
+__device__ __forceinline__ bool clear_dead(const RowLoop& w, int i, int k0, uint32_t bad) {
+    if (k0 + BN <= w.len && !bad) return true;
+    const int at = w.nv + i, row = ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31);
+    const bool ok = mbar_wait_warp(w.sbase + BAR_VF + 8 * (at & 1), (at >> 1) & 1, kWaitLimit);
+    if (k0 + row >= w.len || ((bad >> (row >> w.lb)) & 1u)) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) st_shared_v4(w.sbase + SM_V + (at & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    return ok;
+}
+
+// The blocks of a warp without rows that look scores up.
+__device__ __noinline__ RowResult plain_rows(const RowLoop w) {
+    const uint32_t tS = w.tmem, tO = w.tmem + TO_COL, tP = w.tmem + TP_COL;
+    float m = kNegInf, l = 0.f;
+    for (int i = 0; i < w.nt; ++i) {
+        const int k0 = w.k_first - i * BN;
+        uint32_t bad;
+        if (!block_arrived(w, i, bad)) return {m, l, false};
+        if (k0 + BN > w.vmin || bad) {
+            if (!p_free(w, i)) return {m, l, false};
+            const float2 ml = mixed_block(m, l, Patterns{}, w.unit, w.vis, w.keyed, i == 0, tS, tO, tP, k0, w.len, bad, w.lb);
+            m = ml.x;
+            l = ml.y;
+            if (w.keyed) {
+                tc_fence_before();
+                mbar_arrive_warp(w.sbase + BAR_SF);
+            }
+            if (!clear_dead(w, i, k0, bad)) return {m, l, false};
+        } else {
+            uint32_t v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+            tmem_wait_ld();
+            tc_fence_before();
+            if (w.keyed) mbar_arrive_warp(w.sbase + BAR_SF);  // the MMA warp may now overwrite S
+            const float mx = row_max(v);
+            float f = 1.f;
+            if ((mx - m) * w.unit > 8.f) {
+                f = ex2((m - mx) * w.unit);
+                l *= f;
+                m = mx;
+            }
+            if (!p_free(w, i)) return {m, l, false};
+            const float nm = m == kNegInf ? 0.f : -m * w.unit;
+            const uint64_t unit2 = f32x2(w.unit, w.unit), nm2 = f32x2(nm, nm);
+            uint64_t l2[4] = {0, 0, 0, 0};
+            exp_quarter<0>(v, unit2, nm2, l2, tP);
+            exp_quarter<1>(v, unit2, nm2, l2, tP);
+            exp_quarter<2>(v, unit2, nm2, l2, tP);
+            exp_quarter<3>(v, unit2, nm2, l2, tP);
+            const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
+            l += s2.x + s2.y;
+            if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
+        }
+        hand_over(w);
+    }
+    return {m, l, true};
+}
+
+// The blocks of a warp with replaced rows.  pure: all its rows with a token are, of
+// one head; near: their stretches of r lie together (low, off: see near_block).
+__device__ __noinline__ RowResult pattern_rows(const RowLoop w, const Patterns pt, const FarRows far, bool pure, bool near,
+                                               int low, int off) {
+    const uint32_t tS = w.tmem, tO = w.tmem + TO_COL, tP = w.tmem + TP_COL;
+    float m = kNegInf, l = 0.f;
+    bool primed = false, ok = true;
+    for (int i = 0; ok && i < w.nt; ++i) {
+        const int k0 = w.k_first - i * BN;
+        uint32_t bad;
+        ok = block_arrived(w, i, bad) && p_free(w, i);
+        if (!ok) break;
+        float2 ml;
+        if (pure && k0 + BN <= w.vmin && !bad) {
+            const bool next = i + 1 < w.nt;
+            ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off, tO, tP, k0)
+                      : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
+            primed = next;
+        } else {
+            if (primed) {  // copies begun for this block: its staging area is wanted
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                __syncwarp();
+                primed = false;
+            }
+            ml = mixed_block(m, l, pt, w.unit, w.vis, w.keyed, i == 0, tS, tO, tP, k0, w.len, bad, w.lb);
+        }
+        m = ml.x;
+        l = ml.y;
+        if (w.keyed) {
+            tc_fence_before();
+            mbar_arrive_warp(w.sbase + BAR_SF);
+        }
+        ok = clear_dead(w, i, k0, bad);
+        hand_over(w);
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncwarp();
+    return {m, l, ok};
+}
+
 template <bool PREFIX>
 __global__ void __launch_bounds__(NTHREADS, 2)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ PagedParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t bar_kf = sbase + SM_BAR, bar_ke = bar_kf + 8 * NST;    // [NST] K stage full, free (S MMA done)
-    const uint32_t bar_vf = bar_ke + 8 * NST, bar_ve = bar_vf + 8 * NST;  // [NST] V stage full, free (P V MMA done)
-    const uint32_t bar_item = bar_ve + 8 * NST, bar_taken = bar_item + 16;  // [2] item slot full, free (MMA and row warps)
-    const uint32_t bar_q = bar_taken + 16;                              // queries in place (4 warp arrivals)
-    const uint32_t bar_s = bar_q + 8;                                   // S ready
-    const uint32_t bar_sf = bar_s + 8;                                  // S copied out by the rows (4 warp arrivals)
-    const uint32_t bar_p = bar_sf + 8;                                  // P written (4 warp arrivals)
-    const uint32_t bar_o = bar_p + 8;                                   // P V done
-    const uint32_t bar_join = bar_o + 8;                                // row warps together (4 warp arrivals)
+    const uint32_t bar_kf = sbase + BAR_KF, bar_ke = sbase + BAR_KE, bar_vf = sbase + BAR_VF, bar_ve = sbase + BAR_VE;
+    const uint32_t bar_item = sbase + BAR_ITEM, bar_taken = sbase + BAR_TAKEN, bar_q = sbase + BAR_Q, bar_s = sbase + BAR_S;
+    const uint32_t bar_sf = sbase + BAR_SF, bar_p = sbase + BAR_P, bar_o = sbase + BAR_O, bar_join = sbase + BAR_JOIN;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SM_MISC);
     volatile int* last_flag = reinterpret_cast<int*>(smem + SM_MISC + 4);
-    volatile uint32_t *kmeta = reinterpret_cast<uint32_t*>(smem + SM_MISC + 8), *vmeta = kmeta + 4;
+    volatile uint32_t *kmeta = reinterpret_cast<uint32_t*>(smem + SM_KMETA),
+                      *vmeta = reinterpret_cast<uint32_t*>(smem + SM_VMETA);
     TcPiece* items = reinterpret_cast<TcPiece*>(smem + SM_ITEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (sbase & 1023u) {  // the swizzled tiles need what the declaration asks for
@@ -521,8 +675,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     } else {
         // ------------------------------------------------ row threads
         const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + TO_COL, tP = tmem + lane_off + TP_COL;
+        const uint32_t tmem_rows = tmem + ((uint32_t)(quarter * 32) << 16), tO = tmem_rows + TO_COL;
         const int lb = min(p.log_page, 7);
         int nk = 0, nv = 0, joins = 0;  // S and P V products, joins of the row warps so far
         bool ok = true, waited = false;
@@ -555,92 +708,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 mbar_arrive_warp(bar_q);
             }
             const bool rep = info.out >= 0 && info.replaced;
-            const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : INT_MAX);
             const uint32_t reps = __ballot_sync(~0u, rep && info.vis > 0);
-            const float unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
-            float m = kNegInf, l = 0.f;  // running maximum (in the row's units), sum
-            // Block i has landed, with its scores where it has some; boxes without a page in `bad`.
-            auto arrived = [&](int i, uint32_t& bad) {
-                if (keyed) {
-                    // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load
-                    // was seen by the MMA warp before it issued S)
-                    ok = mbar_wait_warp(bar_s, nk & 1, kWaitLimit);
-                    bad = kmeta[nk & 3];
-                    ++nk;
-                } else {
-                    ok = mbar_wait_warp(bar_vf + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
-                    bad = vmeta[nv & 3];
-                }
-                tc_fence_after();
-                return ok;
-            };
-            // P V of the block before has read P and added to O.
-            auto p_free = [&](int i) {
-                if (i == 0) return true;
-                ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
-                tc_fence_after();
-                return ok;
-            };
-            // P of the block is in place.  Slots without a token may hold a NaN, and 0 times that is one: their V rows
-            // become zeros first.
-            auto hand_over = [&](int k0, uint32_t bad) {
-                if (k0 + BN > x.len || bad) {
-                    ok = mbar_wait_warp(bar_vf + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
-                    if (k0 + row >= x.len || ((bad >> (row >> lb)) & 1u)) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            st_shared_v4(sbase + SM_V + (nv & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive_warp(bar_p);
-                ++nv;
-                return ok;
-            };
+            RowLoop w;
+            w.sbase = sbase;
+            w.tmem = tmem_rows;
+            w.nt = x.nt;
+            w.k_first = (x.t0 + x.nt - 1) * BN;
+            w.len = x.len;
+            w.nk = nk;
+            w.nv = nv;
+            w.lb = lb;
+            w.vis = info.vis;
+            // (a warp without rows still clears its share of the dead slots)
+            w.vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : x.len);
+            w.unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
+            w.keyed = keyed;
+            RowResult res;  // running maximum (in the row's units), sum
             if (!reps) {
-                for (int i = 0; i < x.nt; ++i) {
-                    const int k0 = (x.t0 + x.nt - 1 - i) * BN;
-                    uint32_t bad;
-                    if (!arrived(i, bad)) break;
-                    if (k0 + BN > vmin || bad) {
-                        if (!p_free(i)) break;
-                        const float2 ml = mixed_block(m, l, Patterns{}, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, x.len, bad, lb);
-                        m = ml.x;
-                        l = ml.y;
-                        if (keyed) {
-                            tc_fence_before();
-                            mbar_arrive_warp(bar_sf);
-                        }
-                    } else {
-                        uint32_t v[128];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-                        tmem_wait_ld();
-                        tc_fence_before();
-                        if (keyed) mbar_arrive_warp(bar_sf);  // the MMA warp may now overwrite S
-                        const float mx = row_max(v);
-                        float f = 1.f;
-                        if ((mx - m) * unit > 8.f) {
-                            f = ex2((m - mx) * unit);
-                            l *= f;
-                            m = mx;
-                        }
-                        if (!p_free(i)) break;
-                        const float nm = m == kNegInf ? 0.f : -m * unit;
-                        const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
-                        uint64_t l2[4] = {0, 0, 0, 0};
-                        exp_quarter<0>(v, unit2, nm2, l2, tP);
-                        exp_quarter<1>(v, unit2, nm2, l2, tP);
-                        exp_quarter<2>(v, unit2, nm2, l2, tP);
-                        exp_quarter<3>(v, unit2, nm2, l2, tP);
-                        const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
-                        l += s2.x + s2.y;
-                        if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
-                    }
-                    if (!hand_over(k0, bad)) break;
-                }
+                res = plain_rows(w);
             } else {
                 const int head = max(info.replaced - 1, 0);
                 const bool looks = (reps >> lane) & 1u;
@@ -664,8 +749,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const int low = __reduce_min_sync(~0u, off);
                 pt.span = __reduce_max_sync(~0u, off) - low;
                 const bool near = pt.span <= NEAR_SPAN;
-                FarRows far;
-                bool primed = false;
+                FarRows far{};
                 if (pure && !near) {
                     // the stretch of the 16 keys from key k on begins 15 floats before r's entry of key k
                     const long long start = r_first + off - 15;
@@ -676,39 +760,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     far.src[4] = edge + 16;
                     far.room = (long long)p.H * p.pattern_len - (r_first + edge + 16);
                 }
-                for (int i = 0; i < x.nt; ++i) {
-                    const int k0 = (x.t0 + x.nt - 1 - i) * BN;
-                    uint32_t bad;
-                    if (!arrived(i, bad) || !p_free(i)) break;
-                    float2 ml;
-                    if (pure && k0 + BN <= vmin && !bad) {
-                        const bool next = i + 1 < x.nt;
-                        ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off - low, tO, tP, k0)
-                                  : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
-                        primed = next;
-                    } else {
-                        if (primed) {  // copies begun for this block: its staging area is wanted
-                            asm volatile("cp.async.wait_all;\n" ::: "memory");
-                            __syncwarp();
-                            primed = false;
-                        }
-                        ml = mixed_block(m, l, pt, unit, info.vis, keyed, i == 0, tS, tO, tP, k0, x.len, bad, lb);
-                    }
-                    m = ml.x;
-                    l = ml.y;
-                    if (keyed) {
-                        tc_fence_before();
-                        mbar_arrive_warp(bar_sf);
-                    }
-                    if (!hand_over(k0, bad)) break;
-                }
-                asm volatile("cp.async.wait_all;\n" ::: "memory");
-                __syncwarp();
+                res = pattern_rows(w, pt, far, pure, near, low, off - low);
             }
+            ok = res.ok;
+            nv += x.nt;
+            if (keyed) nk += x.nt;
+            const float m = rep ? res.m : 0.125f * res.m, l = res.l;
             if (ok && x.nt > 0) ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
             tc_fence_after();
             if (!ok) break;
-            if (!rep) m *= 0.125f;
             if (!PREFIX && p.prefix.part && !waited) {
                 griddep_wait();
                 waited = true;
