@@ -58,19 +58,52 @@ static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4 && PAT_BYTES >= 2 * NEAR_BUF * 4, 
 constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;   // [4 warps] staging area
 constexpr uint32_t SM_ROW = SM_PAT + 4 * PAT_BYTES;  // [128] {head, r at local key 0 within the head's} of a row
 constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
-constexpr uint32_t SM_ITEM = SM_BAR + 20 * 8;  // [2] TcPiece
-constexpr uint32_t SM_MISC = SM_ITEM + 2 * 48;  // TMEM address, last flag, [4] boxes of a K load without a page, [4] of a V load
+constexpr uint32_t SM_ITEM = SM_BAR + 20 * 8;       // [2] TcPiece
+constexpr uint32_t SM_WARP = SM_ITEM + 2 * 48;      // [4] WarpRows
+constexpr uint32_t SM_MISC = SM_WARP + 4 * 80;      // TMEM address, last flag, [4] boxes of a K load without a page, [4] of a V load
 constexpr uint32_t SM_TOTAL = SM_MISC + 40;
 
 struct TcAxis {
     static constexpr int kTile = BN, kTileKeyless = BN, kItem = 2, kSnap = 2, kMinUnits = 8;
 };
 // An item's stretch as the other warps need it: nt blocks from t0 (those that some
-// row sees), keyed: some row is ordinary.
+// row sees; nt < 0: no more items), keyed: some row is ordinary.
 struct TcPiece {
-    int b, gi, rb, len, t0, nt, keyed, pieces, c_first;  // nt < 0: no more
+    int b, gi, rb, len, t0, nt, keyed, pieces, c_first, lb;  // lb: log2 of the rows of a box
 };
 static_assert(sizeof(TcPiece) <= 48, "item slot");
+// What the rows of a warp have in common.  It and the item stay in shared memory
+// and are read where they are wanted: the row loops below are functions of their
+// own, with a handful of scalar arguments, so that nothing crowds the 128 scores of
+// a row out of the registers or goes through the stack (with two CTAs' shared
+// memory taken, L1 is too small to hold one: spilled, the loops took twice as long).
+struct WarpRows {
+    const float *a, *r;    // of the head of the first row that looks scores up, at local key 0 (r: at its own position, r[-j])
+    const float *a0, *r0;  // the arrays, a0 at local key 0 of head 0
+    int pattern_len;
+    uint32_t reps;         // the rows that look their scores up
+    int one_head;          // all of these are of one head
+    int pure;              // all rows with a token look up, by one head's vectors
+    int low, span;         // from r on: the lowest of their stretches, and from there to the highest
+    int room;              // floats of the array past r
+    int vmin;              // keys that every row sees
+};
+static_assert(sizeof(WarpRows) <= 80, "warp slot");
+struct RowResult {
+    float m, l;
+    int ok;
+};
+
+__device__ __forceinline__ uint8_t* smem_base() {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    return smem;
+}
+__device__ __forceinline__ int quarter_of() { return (threadIdx.x >> 5) & 3; }
+__device__ __forceinline__ const volatile TcPiece& item_of(int ni) {
+    return reinterpret_cast<volatile TcPiece*>(smem_base() + SM_ITEM)[ni & 1];
+}
+__device__ __forceinline__ const WarpRows& warp_rows() { return reinterpret_cast<WarpRows*>(smem_base() + SM_WARP)[quarter_of()]; }
+__device__ __forceinline__ float* staging() { return reinterpret_cast<float*>(smem_base() + SM_PAT + quarter_of() * PAT_BYTES); }
 
 // Row max of 128 raw scores: three-input max, four independent chains.
 __device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
@@ -109,18 +142,6 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
         tmem_st32(tO + 32 * c, ov);
     }
 }
-
-// What a warp's rows look scores up by.
-struct Patterns {
-    const float *a, *r;    // of the head of the warp's first replaced row, at local key 0 (r: at its own position, pr[-j])
-    const float *a0, *r0;  // the arrays, a0 at local key 0 of head 0
-    int pattern_len;
-    const int2* rows;  // {head, r at local key 0 within the head's} of the warp's rows
-    float* pat;        // the warp's staging area
-    uint32_t reps;     // the warp's rows that look their scores up
-    int span;          // from the lowest of their stretches of r to the highest
-    bool one_head;     // all of these are of one head
-};
 
 // Scores of 32 keys, chunk c of a block (which goes from 3 to 0), of a row each:
 // the maximum moves if it must (then what the block has written of P so far is
@@ -187,86 +208,83 @@ __device__ __forceinline__ void add_a(float* v, const float* a) {
 
 // A block of a warp whose rows are all replaced, of one head, and see every key of
 // it, their stretches of r at most NEAR_SPAN apart: one stretch serves them all,
-// copied a block ahead.  low: the lowest row's offset against w.r, off: this one's
-// against that.  primed: the block's copies are under way; next: the block after it
-// is of this kind, and its copies are started.  Returns (m, l).
-__device__ __forceinline__ void near_copy(const Patterns& w, int low, int k0) {
+// copied a block ahead.  off: this row's against the lowest.  primed: the block's
+// copies are under way; next: the block after it is of this kind, and its copies
+// are started.  Returns (m, l).
+__device__ __forceinline__ void near_copy(int k0) {
+    const WarpRows& w = warp_rows();
     const int lane = threadIdx.x & 31;
-    const uint32_t buf = smem_addr(w.pat) + (uint32_t)((k0 / BN) & 1) * NEAR_BUF * 4;
+    const uint32_t buf = smem_addr(staging()) + (uint32_t)((k0 / BN) & 1) * NEAR_BUF * 4;
+    const float *a = w.a + k0 + lane, *r = w.r + w.low - k0 - 127;  // r of the lowest row's last key
+    const int most = w.span + 127;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, w.a + k0 + 32 * i + lane);
-    const float* r = w.r + low - k0 - 127;  // r of the lowest row's last key
+    for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, a + 32 * i);
 #pragma unroll
-    for (int i = 0; i < (128 + NEAR_SPAN) / 32; ++i) copy4(buf + (128 + 32 * i + lane) * 4, r + min(32 * i + lane, w.span + 127));
+    for (int i = 0; i < (128 + NEAR_SPAN) / 32; ++i) copy4(buf + (128 + 32 * i + lane) * 4, r + min(32 * i + lane, most));
     copies_commit();
 }
-__device__ __noinline__ float2 near_block(float m, float l, const Patterns w, bool primed, bool next, bool first, int low,
-                                          int off, uint32_t tO, uint32_t tP, int k0) {
-    if (!primed) near_copy(w, low, k0);
+__device__ __noinline__ float2 near_block(float m, float l, bool primed, bool next, bool first, int off, uint32_t tmem, int k0) {
+    if (!primed) near_copy(k0);
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncwarp();
-    if (next) near_copy(w, low, k0 - BN);
-    const float *a = w.pat + ((k0 / BN) & 1) * NEAR_BUF, *r = a + 128 + 127 + off;
+    if (next) near_copy(k0 - BN);
+    const float *a = staging() + ((k0 / BN) & 1) * NEAR_BUF, *r = a + 128 + 127 + off;
 #pragma unroll 1
     for (int c = 3; c >= 0; --c) {
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = r[-32 * c - e];
         add_a<32>(v, a + 32 * c);
-        chunk_out(v, c, first, kLog2e, m, l, tO, tP);
+        chunk_out(v, c, first, kLog2e, m, l, tmem + TO_COL, tmem + TP_COL);
     }
     __syncwarp();  // the buffer has been read
     return make_float2(m, l);
 }
 
-// The same where they lie anywhere: 16 keys at a time, three under way.  src[i]:
-// where this lane's i-th 16 bytes of the stretch from local key 0 on lie against
-// w.r (rows 8 i + lane / 4; src[4]: the fifth of its own row, with the floats of r
-// that are left from there on in `room`); shift: floats between the boundary and
-// the row's stretch.
-struct FarRows {
-    int src[5];
-    int shift;
-    long long room;
-};
-__device__ __forceinline__ void far_copy(const Patterns& w, const FarRows& f, int key) {  // the 16 keys from `key` on
+// The same where they lie anywhere: 16 keys at a time, three under way.  The 16
+// bytes i = 0..3 that a lane copies are of the rows 8 i + lane / 4, the fifth of its
+// own row.  off: this row's stretch against the warp's first, edge: the 16-byte
+// boundary at or before its 16 entries from local key 15 down to key 0.
+__device__ __forceinline__ void far_copy(int edge, int key) {  // the 16 keys from `key` on
+    const WarpRows& w = warp_rows();
     const int lane = threadIdx.x & 31;
-    const uint32_t buf = smem_addr(w.pat) + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF * 4;
+    const uint32_t buf = smem_addr(staging()) + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF * 4;
+    const float *r = w.r - key, *a = w.a + key;
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
         const uint32_t dst = buf + (i < 4 ? (8 * i + (lane >> 2)) * FAR_PITCH + 4 * (lane & 3) : lane * FAR_PITCH + 16) * 4;
+        const int src = i < 4 ? __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3) : edge + 16;
         // the fifth may end past the array's last float, or begin there (a stretch that starts on a boundary needs none)
-        const int bytes = i < 4 ? 16 : (int)min(16ll, max(0ll, (f.room + key) * 4));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(w.r + f.src[i] - key), "r"(bytes));
+        const int bytes = i < 4 ? 16 : min(4, max(0, w.room + key - src)) * 4;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(r + src), "r"(bytes));
     }
-    if (lane < 16) copy4(buf + (FAR_A + lane) * 4, w.a + key + lane);
+    if (lane < 16) copy4(buf + (FAR_A + lane) * 4, a + lane);
     copies_commit();
 }
-__device__ __noinline__ float2 far_block(float m, float l, const Patterns w, const FarRows f, bool primed, bool next,
-                                         bool first, uint32_t tO, uint32_t tP, int k0) {
+__device__ __noinline__ float2 far_block(float m, float l, bool primed, bool next, bool first, int off, int edge,
+                                         uint32_t tmem, int k0) {
     const int lane = threadIdx.x & 31;
     if (!primed) {
 #pragma unroll 1
-        for (int n = 7; n > 7 - FAR_BUFS; --n) far_copy(w, f, k0 + 16 * n);
+        for (int n = 7; n > 7 - FAR_BUFS; --n) far_copy(edge, k0 + 16 * n);
     }
+    const float* rows = staging() + lane * FAR_PITCH + (off - edge);
 #pragma unroll 1
     for (int c = 3; c >= 0; --c) {
         float v[32];
 #pragma unroll
         for (int h = 1; h >= 0; --h) {
-            const int n = 2 * c + h, key = k0 + 16 * n;
+            const int n = 2 * c + h, key = k0 + 16 * n, buf = ((key >> 4) % FAR_BUFS) * FAR_BUF;
             asm volatile("cp.async.wait_group %0;\n" ::"n"(FAR_BUFS - 1) : "memory");
             __syncwarp();
-            const float* buf = w.pat + (uint32_t)((key >> 4) % FAR_BUFS) * FAR_BUF;
-            const float* src = buf + lane * FAR_PITCH + f.shift + 15;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[16 * h + e] = src[-e];
-            add_a<16>(v + 16 * h, buf + FAR_A);
+            for (int e = 0; e < 16; ++e) v[16 * h + e] = rows[buf - e];
+            add_a<16>(v + 16 * h, staging() + buf + FAR_A);
             __syncwarp();
-            if (n >= FAR_BUFS || next) far_copy(w, f, key - 16 * FAR_BUFS);
+            if (n >= FAR_BUFS || next) far_copy(edge, key - 16 * FAR_BUFS);
             else copies_commit();
         }
-        chunk_out(v, c, first, kLog2e, m, l, tO, tP);
+        chunk_out(v, c, first, kLog2e, m, l, tmem + TO_COL, tmem + TP_COL);
     }
     return make_float2(m, l);
 }
@@ -274,43 +292,48 @@ __device__ __noinline__ float2 far_block(float m, float l, const Patterns w, con
 // A block of a warp that is neither that nor plain: it holds both kinds, or there are
 // keys that a row does not see.  32 keys at a time, in a loop (a cold unrolled
 // copy would cost more to fetch than to run).  Returns (m, l).
-__device__ __noinline__ float2 mixed_block(float m, float l, const Patterns w, float unit, int vis, bool keyed, bool first,
-                                           uint32_t tS, uint32_t tO, uint32_t tP, int k0, int len, uint32_t bad, int lb) {
-    const int lane = threadIdx.x & 31;
-    const bool rep = (w.reps >> lane) & 1u;
+__device__ __noinline__ float2 mixed_block(float m, float l, float unit, int vis, bool first, uint32_t tmem, int ni, int k0,
+                                           uint32_t bad) {
+    const WarpRows& w = warp_rows();
+    const int lane = threadIdx.x & 31, len = item_of(ni).len, lb = item_of(ni).lb;
+    const bool keyed = item_of(ni).keyed;
+    const uint32_t reps = w.reps;
     const int vis_last = max(vis, 1) - 1;
+    float* pat = staging();
+    const int2* rows = reinterpret_cast<const int2*>(smem_base() + SM_ROW) + quarter_of() * 32;
 #pragma unroll 1
     for (int c = 3; c >= 0; --c) {
         uint32_t raw[32];
         float v[32];
         if (keyed) {
-            tmem_ld32(tS + 32 * c, raw);
+            tmem_ld32(tmem + 32 * c, raw);
             tmem_wait_ld();
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
-        if (w.reps) {
+        if (reps) {
             const int key = k0 + 32 * c + lane;
-            const float av = w.one_head ? __ldg(w.a + min(key, len - 1)) : 0.f;
+            const bool one = w.one_head;
+            const float av = one ? __ldg(w.a + min(key, len - 1)) : 0.f;
 #pragma unroll
             for (int r0 = 0; r0 < 32; r0 += 8) {
-                if (!((w.reps >> r0) & 0xffu)) continue;
+                if (!((reps >> r0) & 0xffu)) continue;
                 float x[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {  // (a row that looks nothing up reads entry 0)
                     const int j = min(key, __shfl_sync(~0u, vis_last, r0 + u));
-                    const int2 at = w.rows[r0 + u];
-                    const bool read = (w.reps >> (r0 + u)) & 1u;
+                    const int2 at = rows[r0 + u];
+                    const bool read = (reps >> (r0 + u)) & 1u;
                     const long long ph = (long long)at.x * w.pattern_len;
-                    x[u] = (w.one_head ? av : __ldg(read ? w.a0 + ph + j : w.a)) + __ldg(read ? w.r0 + ph + at.y - j : w.r);
+                    x[u] = (one ? av : __ldg(read ? w.a0 + ph + j : w.a)) + __ldg(read ? w.r0 + ph + at.y - j : w.r);
                 }
 #pragma unroll
-                for (int u = 0; u < 8; ++u) w.pat[(r0 + u) * PAT_PITCH + lane] = x[u];
+                for (int u = 0; u < 8; ++u) pat[(r0 + u) * PAT_PITCH + lane] = x[u];
             }
             __syncwarp();
-            if (rep) {
+            if ((reps >> lane) & 1u) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = w.pat[lane * PAT_PITCH + e];
+                for (int e = 0; e < 32; ++e) v[e] = pat[lane * PAT_PITCH + e];
             }
             __syncwarp();
         }
@@ -318,7 +341,7 @@ __device__ __noinline__ float2 mixed_block(float m, float l, const Patterns w, f
 #pragma unroll
         for (int e = 0; e < 32; ++e)
             if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = kNegInf;
-        chunk_out(v, c, first, unit, m, l, tO, tP);
+        chunk_out(v, c, first, unit, m, l, tmem + TO_COL, tmem + TP_COL);
     }
     return make_float2(m, l);
 }
@@ -336,129 +359,116 @@ constexpr uint32_t BAR_JOIN = BAR_O + 8;                            // row warps
 static_assert(BAR_JOIN + 8 <= SM_ITEM, "barrier area");
 constexpr uint32_t SM_KMETA = SM_MISC + 8, SM_VMETA = SM_MISC + 24;
 
-// The blocks of an item as a row warp goes through them: nt blocks, the first of
-// which begins at key k_first (they go down from there).  nk, nv: S and P V
-// products before it.  The two loops below are functions of their own so that
-// what an item needs otherwise does not crowd the 128 scores out of the registers
-// (spilled, the loop took twice as long).
-struct RowLoop {
-    uint32_t sbase, tmem;  // tmem: of this warp's lanes
-    int nt, k_first, len, nk, nv, lb, vis, vmin;
-    float unit;
-    bool keyed;
-};
-struct RowResult {
-    float m, l;
+// Block i of item ni has landed, with its scores where it has some; boxes without a
+// page in `bad`.  nk, nv: S and P V products before it.
+__device__ __forceinline__ bool block_arrived(int ni, int nk, int nv, uint32_t& bad) {
+    const uint32_t sbase = smem_addr(smem_base());
     bool ok;
-};
-// Block i has landed, with its scores where it has some; boxes without a page in `bad`.
-__device__ __forceinline__ bool block_arrived(const RowLoop& w, int i, uint32_t& bad) {
-    bool ok;
-    if (w.keyed) {
+    if (item_of(ni).keyed) {
         // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load was
         // seen by the MMA warp before it issued S)
-        ok = mbar_wait_warp(w.sbase + BAR_S, (w.nk + i) & 1, kWaitLimit);
-        bad = ld_shared_u32(w.sbase + SM_KMETA + 4 * ((w.nk + i) & 3));
+        ok = mbar_wait_warp(sbase + BAR_S, nk & 1, kWaitLimit);
+        bad = ld_shared_u32(sbase + SM_KMETA + 4 * (nk & 3));
     } else {
-        const int at = w.nv + i;
-        ok = mbar_wait_warp(w.sbase + BAR_VF + 8 * (at & 1), (at >> 1) & 1, kWaitLimit);
-        bad = ld_shared_u32(w.sbase + SM_VMETA + 4 * (at & 3));
+        ok = mbar_wait_warp(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+        bad = ld_shared_u32(sbase + SM_VMETA + 4 * (nv & 3));
     }
     tc_fence_after();
     return ok;
 }
 // P V of the block before has read P and added to O (an item's first: waited for by the item before).
-__device__ __forceinline__ bool p_free(const RowLoop& w, int i) {
-    if (i == 0) return true;
-    const bool ok = mbar_wait_warp(w.sbase + BAR_O, (w.nv + i - 1) & 1, kWaitLimit);
+__device__ __forceinline__ bool p_free(bool first, int nv) {
+    if (first) return true;
+    const bool ok = mbar_wait_warp(smem_addr(smem_base()) + BAR_O, (nv - 1) & 1, kWaitLimit);
     tc_fence_after();
     return ok;
 }
-__device__ __forceinline__ void hand_over(const RowLoop& w) {
+__device__ __forceinline__ void s_copied(int ni) {  // the MMA warp may now overwrite S
+    tc_fence_before();
+    if (item_of(ni).keyed) mbar_arrive_warp(smem_addr(smem_base()) + BAR_SF);
+}
+__device__ __forceinline__ void hand_over() {
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive_warp(w.sbase + BAR_P);
+    mbar_arrive_warp(smem_addr(smem_base()) + BAR_P);
 }
 // Slots without a token may hold a NaN, and 0 times that is one: their V rows become
 // zeros before P V reads them.
-__device__ __forceinline__ bool clear_dead(const RowLoop& w, int i, int k0, uint32_t bad) {
-    if (k0 + BN <= w.len && !bad) return true;
-    const int at = w.nv + i, row = ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31);
-    const bool ok = mbar_wait_warp(w.sbase + BAR_VF + 8 * (at & 1), (at >> 1) & 1, kWaitLimit);
-    if (k0 + row >= w.len || ((bad >> (row >> w.lb)) & 1u)) {
+__device__ __forceinline__ bool clear_dead(int ni, int nv, int k0, uint32_t bad) {
+    const uint32_t sbase = smem_addr(smem_base());
+    const int len = item_of(ni).len, row = quarter_of() * 32 + (threadIdx.x & 31);
+    if (k0 + BN <= len && !bad) return true;
+    const bool ok = mbar_wait_warp(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+    if (k0 + row >= len || ((bad >> (row >> item_of(ni).lb)) & 1u)) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) st_shared_v4(w.sbase + SM_V + (at & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
+        for (int c = 0; c < 8; ++c) st_shared_v4(sbase + SM_V + (nv & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     return ok;
 }
 
-// The blocks of a warp without rows that look scores up.
-__device__ __noinline__ RowResult plain_rows(const RowLoop w) {
-    const uint32_t tS = w.tmem, tO = w.tmem + TO_COL, tP = w.tmem + TP_COL;
+// The blocks of a warp without rows that look scores up.  tmem: of this warp's lanes.
+__device__ __noinline__ RowResult plain_rows(float unit, int vis, uint32_t tmem, int ni, int nk, int nv) {
     float m = kNegInf, l = 0.f;
-    for (int i = 0; i < w.nt; ++i) {
-        const int k0 = w.k_first - i * BN;
+    int k0 = (item_of(ni).t0 + item_of(ni).nt) * BN;
+    for (int i = 0; i < item_of(ni).nt; ++i, ++nk, ++nv) {
+        k0 -= BN;
         uint32_t bad;
-        if (!block_arrived(w, i, bad)) return {m, l, false};
-        if (k0 + BN > w.vmin || bad) {
-            if (!p_free(w, i)) return {m, l, false};
-            const float2 ml = mixed_block(m, l, Patterns{}, w.unit, w.vis, w.keyed, i == 0, tS, tO, tP, k0, w.len, bad, w.lb);
+        if (!block_arrived(ni, nk, nv, bad)) return {m, l, 0};
+        if (k0 + BN > warp_rows().vmin || bad) {
+            if (!p_free(i == 0, nv)) return {m, l, 0};
+            const float2 ml = mixed_block(m, l, unit, vis, i == 0, tmem, ni, k0, bad);
             m = ml.x;
             l = ml.y;
-            if (w.keyed) {
-                tc_fence_before();
-                mbar_arrive_warp(w.sbase + BAR_SF);
-            }
-            if (!clear_dead(w, i, k0, bad)) return {m, l, false};
+            s_copied(ni);
+            if (!clear_dead(ni, nv, k0, bad)) return {m, l, 0};
         } else {
             uint32_t v[128];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
             tmem_wait_ld();
-            tc_fence_before();
-            if (w.keyed) mbar_arrive_warp(w.sbase + BAR_SF);  // the MMA warp may now overwrite S
+            s_copied(ni);
             const float mx = row_max(v);
             float f = 1.f;
-            if ((mx - m) * w.unit > 8.f) {
-                f = ex2((m - mx) * w.unit);
+            if ((mx - m) * unit > 8.f) {
+                f = ex2((m - mx) * unit);
                 l *= f;
                 m = mx;
             }
-            if (!p_free(w, i)) return {m, l, false};
-            const float nm = m == kNegInf ? 0.f : -m * w.unit;
-            const uint64_t unit2 = f32x2(w.unit, w.unit), nm2 = f32x2(nm, nm);
+            if (!p_free(i == 0, nv)) return {m, l, 0};
+            const float nm = m == kNegInf ? 0.f : -m * unit;
+            const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
             uint64_t l2[4] = {0, 0, 0, 0};
-            exp_quarter<0>(v, unit2, nm2, l2, tP);
-            exp_quarter<1>(v, unit2, nm2, l2, tP);
-            exp_quarter<2>(v, unit2, nm2, l2, tP);
-            exp_quarter<3>(v, unit2, nm2, l2, tP);
+            exp_quarter<0>(v, unit2, nm2, l2, tmem + TP_COL);
+            exp_quarter<1>(v, unit2, nm2, l2, tmem + TP_COL);
+            exp_quarter<2>(v, unit2, nm2, l2, tmem + TP_COL);
+            exp_quarter<3>(v, unit2, nm2, l2, tmem + TP_COL);
             const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
             l += s2.x + s2.y;
-            if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tO, f);
+            if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tmem + TO_COL, f);
         }
-        hand_over(w);
+        hand_over();
     }
-    return {m, l, true};
+    return {m, l, 1};
 }
 
-// The blocks of a warp with replaced rows.  pure: all its rows with a token are, of
-// one head; near: their stretches of r lie together (low, off: see near_block).
-__device__ __noinline__ RowResult pattern_rows(const RowLoop w, const Patterns pt, const FarRows far, bool pure, bool near,
-                                               int low, int off) {
-    const uint32_t tS = w.tmem, tO = w.tmem + TO_COL, tP = w.tmem + TP_COL;
+// The blocks of a warp with replaced rows (off, edge: see near_block and far_block).
+__device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tmem, int ni, int nk, int nv, int off, int edge) {
     float m = kNegInf, l = 0.f;
     bool primed = false, ok = true;
-    for (int i = 0; ok && i < w.nt; ++i) {
-        const int k0 = w.k_first - i * BN;
+    const int nt = item_of(ni).nt;
+    int k0 = (item_of(ni).t0 + nt) * BN;
+    for (int i = 0; ok && i < nt; ++i, ++nk, ++nv) {
+        k0 -= BN;
         uint32_t bad;
-        ok = block_arrived(w, i, bad) && p_free(w, i);
+        ok = block_arrived(ni, nk, nv, bad) && p_free(i == 0, nv);
         if (!ok) break;
+        const WarpRows& w = warp_rows();
         float2 ml;
-        if (pure && k0 + BN <= w.vmin && !bad) {
-            const bool next = i + 1 < w.nt;
-            ml = near ? near_block(m, l, pt, primed, next, i == 0, low, off, tO, tP, k0)
-                      : far_block(m, l, pt, far, primed, next, i == 0, tO, tP, k0);
+        if (w.pure && k0 + BN <= w.vmin && !bad) {
+            const bool next = i + 1 < nt;
+            ml = w.span <= NEAR_SPAN ? near_block(m, l, primed, next, i == 0, off - w.low, tmem, k0)
+                                     : far_block(m, l, primed, next, i == 0, off, edge, tmem, k0);
             primed = next;
         } else {
             if (primed) {  // copies begun for this block: its staging area is wanted
@@ -466,16 +476,13 @@ __device__ __noinline__ RowResult pattern_rows(const RowLoop w, const Patterns p
                 __syncwarp();
                 primed = false;
             }
-            ml = mixed_block(m, l, pt, w.unit, w.vis, w.keyed, i == 0, tS, tO, tP, k0, w.len, bad, w.lb);
+            ml = mixed_block(m, l, unit, vis, i == 0, tmem, ni, k0, bad);
         }
         m = ml.x;
         l = ml.y;
-        if (w.keyed) {
-            tc_fence_before();
-            mbar_arrive_warp(w.sbase + BAR_SF);
-        }
-        ok = clear_dead(w, i, k0, bad);
-        hand_over(w);
+        s_copied(ni);
+        ok = clear_dead(ni, nv, k0, bad);
+        hand_over();
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
     __syncwarp();
@@ -486,7 +493,7 @@ template <bool PREFIX>
 __global__ void __launch_bounds__(NTHREADS, 2)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ PagedParams p) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* const smem = smem_base();
     const uint32_t sbase = smem_addr(smem);
     const uint32_t bar_kf = sbase + BAR_KF, bar_ke = sbase + BAR_KE, bar_vf = sbase + BAR_VF, bar_ve = sbase + BAR_VE;
     const uint32_t bar_item = sbase + BAR_ITEM, bar_taken = sbase + BAR_TAKEN, bar_q = sbase + BAR_Q, bar_s = sbase + BAR_S;
@@ -551,6 +558,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 x.t0 = w.t0;
                 x.pieces = w.pieces;
                 x.c_first = w.c_first;
+                x.lb = lb;
                 const int n = PREFIX ? 0 : new_tokens(p, w.b);
                 int most = 0, ordinary = 0;
 #pragma unroll 1
@@ -676,7 +684,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // ------------------------------------------------ row threads
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t tmem_rows = tmem + ((uint32_t)(quarter * 32) << 16), tO = tmem_rows + TO_COL;
-        const int lb = min(p.log_page, 7);
         int nk = 0, nv = 0, joins = 0;  // S and P V products, joins of the row warps so far
         bool ok = true, waited = false;
         // A barrier of the row warps, bounded like every wait.
@@ -689,8 +696,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
             if (!ok) break;
             const TcPiece x = items[ni & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
             if (x.nt < 0) break;
             const int n_new = PREFIX ? 0 : new_tokens(p, x.b);
             const RowInfo info = row_info<PREFIX>(p, x.b, x.gi, x.len, n_new, p.prefix_len + x.len - n_new, x.rb * BM + row);
@@ -709,58 +714,41 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             const bool rep = info.out >= 0 && info.replaced;
             const uint32_t reps = __ballot_sync(~0u, rep && info.vis > 0);
-            RowLoop w;
-            w.sbase = sbase;
-            w.tmem = tmem_rows;
-            w.nt = x.nt;
-            w.k_first = (x.t0 + x.nt - 1) * BN;
-            w.len = x.len;
-            w.nk = nk;
-            w.nv = nv;
-            w.lb = lb;
-            w.vis = info.vis;
+            const float unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
+            const bool looks = (reps >> lane) & 1u;
+            const int from = reps ? __ffs(reps) - 1 : 0;
+            const long long a_first = __shfl_sync(~0u, info.a0, from), r_first = __shfl_sync(~0u, info.r0, from);
+            const bool one_head = __all_sync(~0u, !looks || info.a0 == a_first);
+            // rows without a token ride along on the first one's stretch
+            const int off = looks && one_head ? (int)(info.r0 - r_first) : 0;
+            const int low = __reduce_min_sync(~0u, off), span = __reduce_max_sync(~0u, off) - low;
+            const int pure = reps && one_head && __all_sync(~0u, info.out < 0 || looks);
             // (a warp without rows still clears its share of the dead slots)
-            w.vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : x.len);
-            w.unit = rep ? kLog2e : 0.125f * kLog2e;  // log2(e) per unit of the row's scores (dot products: 1/8)
-            w.keyed = keyed;
+            const int vmin = __reduce_min_sync(~0u, info.out >= 0 ? info.vis : x.len);
+            const int head = max(info.replaced - 1, 0);
+            reinterpret_cast<int2*>(smem + SM_ROW)[row] = make_int2(head, (int)(info.r0 - (long long)head * p.pattern_len));
+            if (lane == 0) {
+                WarpRows& w = reinterpret_cast<WarpRows*>(smem + SM_WARP)[quarter];
+                w.a = p.a + a_first;
+                w.r = p.r + r_first;
+                w.a0 = p.a + (PREFIX ? 0 : p.prefix_len);
+                w.r0 = p.r;
+                w.pattern_len = p.pattern_len;
+                w.reps = reps;
+                w.one_head = one_head;
+                w.pure = pure;
+                w.low = low;
+                w.span = span;
+                w.room = (int)min((long long)p.H * p.pattern_len - r_first, 1ll << 30);
+                w.vmin = vmin;
+            }
+            __syncwarp();
             RowResult res;  // running maximum (in the row's units), sum
             if (!reps) {
-                res = plain_rows(w);
+                res = plain_rows(unit, info.vis, tmem_rows, ni, nk, nv);
             } else {
-                const int head = max(info.replaced - 1, 0);
-                const bool looks = (reps >> lane) & 1u;
-                const int from = __ffs(reps) - 1;
-                const long long a_first = __shfl_sync(~0u, info.a0, from), r_first = __shfl_sync(~0u, info.r0, from);
-                reinterpret_cast<int2*>(smem + SM_ROW)[row] = make_int2(head, (int)(info.r0 - (long long)head * p.pattern_len));
-                __syncwarp();
-                Patterns pt;
-                pt.reps = reps;
-                pt.a = p.a + a_first;
-                pt.r = p.r + r_first;
-                pt.a0 = p.a + (PREFIX ? 0 : p.prefix_len);
-                pt.r0 = p.r;
-                pt.pattern_len = p.pattern_len;
-                pt.rows = reinterpret_cast<const int2*>(smem + SM_ROW) + quarter * 32;
-                pt.pat = reinterpret_cast<float*>(smem + SM_PAT + quarter * PAT_BYTES);
-                pt.one_head = __all_sync(~0u, !looks || info.a0 == a_first);
-                // all rows with a token look up, by one head's vectors: the others ride along on the first one's
-                const bool pure = pt.one_head && __all_sync(~0u, info.out < 0 || looks);
-                const int off = looks && pt.one_head ? (int)(info.r0 - r_first) : 0;  // (within a head's vector)
-                const int low = __reduce_min_sync(~0u, off);
-                pt.span = __reduce_max_sync(~0u, off) - low;
-                const bool near = pt.span <= NEAR_SPAN;
-                FarRows far{};
-                if (pure && !near) {
-                    // the stretch of the 16 keys from key k on begins 15 floats before r's entry of key k
-                    const long long start = r_first + off - 15;
-                    const int edge = (int)((start & ~3ll) - r_first);
-                    far.shift = (int)(start & 3);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) far.src[i] = __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3);
-                    far.src[4] = edge + 16;
-                    far.room = (long long)p.H * p.pattern_len - (r_first + edge + 16);
-                }
-                res = pattern_rows(w, pt, far, pure, near, low, off - low);
+                const int edge = (int)(((r_first + off - 15) & ~3ll) - r_first);
+                res = pattern_rows(unit, info.vis, tmem_rows, ni, nk, nv, off, edge);
             }
             ok = res.ok;
             nv += x.nt;
@@ -833,6 +821,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
                 join_warps();
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
         }
         if (!ok && lane == 0) report(p.err, 0x503);
     }
