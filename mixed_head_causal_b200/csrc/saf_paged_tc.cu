@@ -18,11 +18,10 @@
 //               2^-8 off, as in the layer's forward), the sum in fp32
 // S_{j+1} is issued as soon as the rows have copied S_j to registers, before P V_j.
 //   ordinary row   s = q . k / 8
-//   replaced row   s = a[j] + r[i - j], 32 keys at a time: a thread reads its own stretch
-//                  of r where the warp's stretches lie together (a chunk's tokens, or
-//                  sequences of one length), else the warp copies the rows' stretches to
-//                  shared memory side by side, asynchronously and 16 bytes at a time, and
-//                  every thread takes its row from there
+//   replaced row   s = a[j] + r[i - j], 32 keys at a time, from shared memory: one stretch
+//                  of r for the whole warp where its rows' stretches lie within NEAR_SPAN of
+//                  each other (a chunk's tokens, sequences of like lengths), else one per row
+//                  (which L2 bounds: a row's own stretch is twice the bytes of a K row)
 // Rows come head by head, a group's ordinary heads first, so that most warps hold
 // one kind, and blocks of replaced rows alone need no K.
 // Per block and row: 128 exponentials against 2 x 128 x 64 multiply-adds, so the exp
@@ -49,12 +48,12 @@ constexpr uint32_t SM_K = SM_Q + TILE_BYTES;
 constexpr uint32_t SM_V = SM_K + NST * TILE_BYTES;
 constexpr int PAT_PITCH = 33;                          // floats: a warp's reads of its 32 rows hit distinct banks
 // A staging area holds three buffers of 16 keys: the stretches of 32 rows of r, from the 16-byte boundary at or
-// before them on (20 floats a row), and a; or two of 128 keys: a, and r from the first to the last row's; or (mixed
-// blocks) the scores of 32 keys of 32 rows.
+// before them on (20 floats a row), and a; or two of 128 keys: a, and one stretch of r that serves all rows, from the
+// 16-byte boundary on; or (mixed blocks) the scores of 32 keys of 32 rows.
 constexpr int FAR_PITCH = 20, FAR_A = 32 * FAR_PITCH, FAR_BUF = FAR_A + 16, FAR_BUFS = 3;
-constexpr int NEAR_SPAN = 64, NEAR_BUF = 128 + 128 + NEAR_SPAN;  // floats; rows at most NEAR_SPAN apart
+constexpr int NEAR_SPAN = 720, NEAR_BUF = 128 + 128 + NEAR_SPAN + 4;  // floats; rows at most NEAR_SPAN apart
 constexpr uint32_t PAT_BYTES = FAR_BUFS * FAR_BUF * 4;  // a warp's staging area
-static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4 && PAT_BYTES >= 2 * NEAR_BUF * 4, "all uses fit");
+static_assert(PAT_BYTES >= 32 * PAT_PITCH * 4 && PAT_BYTES >= 2 * NEAR_BUF * 4 && NEAR_BUF % 4 == 0, "all uses fit");
 constexpr uint32_t SM_PAT = SM_V + NST * TILE_BYTES;   // [4 warps] staging area
 constexpr uint32_t SM_ROW = SM_PAT + 4 * PAT_BYTES;  // [128] {head, r at local key 0 within the head's} of a row
 constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
@@ -85,6 +84,7 @@ struct WarpRows {
     int one_head;          // all of these are of one head
     int pure;              // all rows with a token look up, by one head's vectors
     int low, span;         // from r on: the lowest of their stretches, and from there to the highest
+    int low_edge;          // the 16-byte boundary at or before the lowest's entry of local key 127
     int room;              // floats of the array past r
     int vmin;              // keys that every row sees
 };
@@ -207,20 +207,23 @@ __device__ __forceinline__ void add_a(float* v, const float* a) {
 }
 
 // A block of a warp whose rows are all replaced, of one head, and see every key of
-// it, their stretches of r at most NEAR_SPAN apart: one stretch serves them all,
-// copied a block ahead.  off: this row's against the lowest.  primed: the block's
-// copies are under way; next: the block after it is of this kind, and its copies
-// are started.  Returns (m, l).
+// it, their stretches of r at most NEAR_SPAN apart (a chunk's tokens, sequences of
+// like lengths): one stretch serves them all, copied a block ahead.  off: this
+// row's against the lowest.  primed: the block's copies are under way; next: the
+// block after it is of this kind, and its copies are started.  Returns (m, l).
 __device__ __forceinline__ void near_copy(int k0) {
     const WarpRows& w = warp_rows();
     const int lane = threadIdx.x & 31;
     const uint32_t buf = smem_addr(staging()) + (uint32_t)((k0 / BN) & 1) * NEAR_BUF * 4;
-    const float *a = w.a + k0 + lane, *r = w.r + w.low - k0 - 127;  // r of the lowest row's last key
-    const int most = w.span + 127;
+    const float *a = w.a + k0 + lane, *r = w.r - k0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, a + 32 * i);
-#pragma unroll
-    for (int i = 0; i < (128 + NEAR_SPAN) / 32; ++i) copy4(buf + (128 + 32 * i + lane) * 4, r + min(32 * i + lane, most));
+    // from the boundary at or before the lowest row's last key to the highest row's first key
+    const int edge = w.low_edge, stop = w.low + w.span + 1;
+    for (int at = edge + 4 * lane; at < stop; at += 128) {
+        const int bytes = min(4, w.room + k0 - at) * 4;  // (the last may reach past the array)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(buf + (128 + at - edge) * 4), "l"(r + at), "r"(bytes));
+    }
     copies_commit();
 }
 __device__ __noinline__ float2 near_block(float m, float l, bool primed, bool next, bool first, int off, uint32_t tmem, int k0) {
@@ -228,7 +231,7 @@ __device__ __noinline__ float2 near_block(float m, float l, bool primed, bool ne
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncwarp();
     if (next) near_copy(k0 - BN);
-    const float *a = staging() + ((k0 / BN) & 1) * NEAR_BUF, *r = a + 128 + 127 + off;
+    const float *a = staging() + ((k0 / BN) & 1) * NEAR_BUF, *r = a + 128 + off - warp_rows().low_edge;
 #pragma unroll 1
     for (int c = 3; c >= 0; --c) {
         float v[32];
@@ -467,7 +470,7 @@ __device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tme
         float2 ml;
         if (w.pure && k0 + BN <= w.vmin && !bad) {
             const bool next = i + 1 < nt;
-            ml = w.span <= NEAR_SPAN ? near_block(m, l, primed, next, i == 0, off - w.low, tmem, k0)
+            ml = w.span <= NEAR_SPAN ? near_block(m, l, primed, next, i == 0, off, tmem, k0)
                                      : far_block(m, l, primed, next, i == 0, off, edge, tmem, k0);
             primed = next;
         } else {
@@ -738,6 +741,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 w.one_head = one_head;
                 w.pure = pure;
                 w.low = low;
+                w.low_edge = (int)(((r_first + low - 127) & ~3ll) - r_first);
                 w.span = span;
                 w.room = (int)min((long long)p.H * p.pattern_len - r_first, 1ll << 30);
                 w.vmin = vmin;
