@@ -395,8 +395,8 @@ saf_status saf_kv_append(const saf_paged_kv* kv, const void* q, const int64_t* q
         if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return SAF_ERR_UNSUPPORTED;
         if (!aligned16(rope) || rope_len < (int64_t)pos_offset + max_len) return SAF_ERR_INVALID_ARG;
     }
-    // eight threads per row, 256 per block, fewer than 2^31 blocks
-    if ((double)B * T * (H + 2 * kv->H_kv) >= 32.0 * INT_MAX) return SAF_ERR_INVALID_ARG;
+    // rows in 31 bits
+    if ((double)B * T * (H + 2 * kv->H_kv) >= INT_MAX - 64.0) return SAF_ERR_INVALID_ARG;
     AppendParams p{};
     if (!copy_strides(k_strides, p.ks) || !copy_strides(v_strides, p.vs) || (q && !copy_strides(q_strides, p.qs)))
         return SAF_ERR_INVALID_ARG;

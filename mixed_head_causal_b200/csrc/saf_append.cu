@@ -26,99 +26,108 @@ __global__ void rope_table_kernel(float* table, int max_pos, int rot_dim, double
     }
 }
 
-// Eight bf16 as fp32, and back (rounded to nearest even).
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+// Two bf16 as a pair of fp32.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) {
+    return tc::f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+// x cos + y sin of a pair, rounded to bf16 (the products and their sum in fp32).
+__device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t y, uint64_t cs, uint64_t sn) {
+    const float2 v = tc::split_f32x2(tc::fma_f32x2(pair_of(x), cs, tc::mul_f32x2(pair_of(y), sn)));
+    return tc::pack_bf16x2(v.x, v.y);
 }
 
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ AppendParams p) {
-    const int R = p.H + 2 * p.kv.H_kv;
-    const int64_t row = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 3;
-    const int c = threadIdx.x & 7;
-    const int64_t tok = row / R;
-    const int rr = (int)(row - tok * R);
-    const int b = (int)(tok / p.T), t = (int)(tok - (int64_t)b * p.T);
-    // lanes of a group agree on everything below, and the shuffle names the group's lanes alone
+// U rows of one token per eight lanes: their loads are in flight together, and the
+// token's position, page and angles are looked up once.  Neighbouring groups of
+// lanes take the same rows of neighbouring tokens, eight at a time: the outputs of a
+// head are then written 1 KB at a stretch.
+template <int U>
+__global__ void __launch_bounds__(256, U == 1 ? 6 : 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    const int unit = blockIdx.x * 4 + (threadIdx.x >> 6), c = threadIdx.x & 7;
+    const int tok8 = p.by_units.div(unit), r0 = (unit - tok8 * p.units) * U;
+    const int tok = tok8 * 8 + ((threadIdx.x >> 3) & 7);
+    const int b = p.by_T.div(tok), t = tok - b * p.T;
+    // the lanes of a group agree on every row and branch below, and the shuffles name the group's lanes alone
     const uint32_t group = 0xffu << (threadIdx.x & 24);
     if (b >= p.B) return;
     const int n = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
-    const int64_t pos = (int64_t)p.seq_lens[b] - n + t;
+    const long long pos = (long long)p.seq_lens[b] - n + t;
     if (t >= n || pos < 0 || pos >= p.max_len) return;
-    const bool isq = rr < p.H, isk = !isq && rr < p.H + p.kv.H_kv;
-    const int h = isq ? rr : isk ? rr - p.H : rr - p.H - p.kv.H_kv;
-    if (isq ? (p.q == nullptr || p.replaced.get(h)) : (isk && p.keyless.get(h))) return;
-    const __nv_bfloat16* src = isq ? p.q + b * p.qs[0] + h * p.qs[1] + t * p.qs[2]
-                               : isk ? p.k + b * p.ks[0] + h * p.ks[1] + t * p.ks[2]
-                                     : p.v + b * p.vs[0] + h * p.vs[1] + t * p.vs[2];
-    uint4 w = *reinterpret_cast<const uint4*>(src + 8 * c);
-    if ((isq || isk) && p.rope) {
-        const int nc = p.rot_dim >> 3, hc = nc >> 1;  // chunks rotated; half of them
-        const float* tab = p.rope + (pos + p.pos_offset) * p.rot_dim;
-        float x[8];
-        unpack8(w, x);
+    // rows [0, H) are q, [H, H + H_kv) k, then v; skipped ones become row -1
+    const int Hkv = p.kv.H_kv;
+    uint4 w[U];
+    int row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int rr = r0 + u, h = rr < p.H ? rr : rr - p.H;
+        const bool skip = rr >= p.H + 2 * Hkv || (rr < p.H ? p.q == nullptr || p.replaced.get(h) : h < Hkv && p.keyless.get(h));
+        row[u] = skip ? -1 : rr;
+        const __nv_bfloat16* src = rr < p.H   ? p.q + b * p.qs[0] + t * p.qs[2] + h * p.qs[1]
+                                   : h < Hkv ? p.k + b * p.ks[0] + t * p.ks[2] + h * p.ks[1]
+                                             : p.v + b * p.vs[0] + t * p.vs[2] + (h - Hkv) * p.vs[1];
+        if (!skip) w[u] = *reinterpret_cast<const uint4*>(src + 8 * c);
+    }
+    const int page = p.page_table[(long long)b * p.max_pages + (pos >> p.log_page)];
+    const int slot = (int)pos & (p.kv.page_size - 1);
+    const bool paged = page >= 0 && page < p.kv.num_pages;
+    const int nc = p.rot_dim >> 3, hc = nc >> 1;  // chunks rotated; half of them
+    // the pairs' angles: y' = x cos + partner sin, with the sine's sign in it
+    uint64_t cs[4], sn[4];
+    int other = c;  // the chunk of the partners (a chunk's own where they lie inside it)
+    if (c < nc) {
+        const float sign = c < hc ? -1.f : 1.f;
+        if (!p.interleaved) other = c < hc ? c + hc : c - hc;
+        const float* tab = p.rope + (pos + p.pos_offset) * p.rot_dim + (p.interleaved ? 4 * c : 8 * (c < hc ? c : other));
+        const float* tab_sin = tab + (p.rot_dim >> 1);
         if (p.interleaved) {
-            if (c < nc) {
-                const float4 cs = *reinterpret_cast<const float4*>(tab + 4 * c);
-                const float4 sn = *reinterpret_cast<const float4*>(tab + (p.rot_dim >> 1) + 4 * c);
-                const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x0 = x[2 * i], x1 = x[2 * i + 1];
-                    x[2 * i] = x0 * cc[i] - x1 * ss[i];
-                    x[2 * i + 1] = x1 * cc[i] + x0 * ss[i];
-                }
-            }
+            const float4 x = __ldg(reinterpret_cast<const float4*>(tab)), y = __ldg(reinterpret_cast<const float4*>(tab_sin));
+            cs[0] = tc::f32x2(x.x, x.x), cs[1] = tc::f32x2(x.y, x.y), cs[2] = tc::f32x2(x.z, x.z), cs[3] = tc::f32x2(x.w, x.w);
+            sn[0] = tc::f32x2(-y.x, y.x), sn[1] = tc::f32x2(-y.y, y.y), sn[2] = tc::f32x2(-y.z, y.z), sn[3] = tc::f32x2(-y.w, y.w);
         } else {
-            const int other = c < hc ? c + hc : c < nc ? c - hc : c;  // the chunk of the pairs' other halves
-            uint4 ow;
-            ow.x = __shfl_sync(group, w.x, other, 8);
-            ow.y = __shfl_sync(group, w.y, other, 8);
-            ow.z = __shfl_sync(group, w.z, other, 8);
-            ow.w = __shfl_sync(group, w.w, other, 8);
-            if (c < nc) {
-                float y[8];
-                unpack8(ow, y);
-                const int i0 = 8 * (c < hc ? c : c - hc);
-                const float sign = c < hc ? -1.f : 1.f;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float4 cs = *reinterpret_cast<const float4*>(tab + i0 + 4 * u);
-                    const float4 sn = *reinterpret_cast<const float4*>(tab + (p.rot_dim >> 1) + i0 + 4 * u);
-                    const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[4 * u + i] = x[4 * u + i] * cc[i] + sign * y[4 * u + i] * ss[i];
-                }
+            for (int i = 0; i < 2; ++i) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(tab) + i);
+                const float4 y = __ldg(reinterpret_cast<const float4*>(tab_sin) + i);
+                cs[2 * i] = tc::f32x2(x.x, x.y), cs[2 * i + 1] = tc::f32x2(x.z, x.w);
+                sn[2 * i] = tc::f32x2(sign * y.x, sign * y.y), sn[2 * i + 1] = tc::f32x2(sign * y.z, sign * y.w);
             }
         }
-        if (c < nc) w = pack8(x);
     }
-    if (isq) {
-        *reinterpret_cast<uint4*>(p.q_out + (((int64_t)b * p.H + h) * p.T + t) * kHeadDim + 8 * c) = w;
-        return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (row[u] < 0) continue;
+        const int rr = row[u], h = rr < p.H ? rr : rr - p.H;
+        if (nc && (rr < p.H || h < Hkv)) {
+            uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w}, y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] = p.interleaved ? __byte_perm(x[i], 0, 0x1032) : __shfl_sync(group, x[i], other, 8);
+            if (c < nc)
+                w[u] = make_uint4(turn(x[0], y[0], cs[0], sn[0]), turn(x[1], y[1], cs[1], sn[1]),
+                                  turn(x[2], y[2], cs[2], sn[2]), turn(x[3], y[3], cs[3], sn[3]));
+        }
+        if (rr < p.H) {
+            *reinterpret_cast<uint4*>(p.q_out + (((long long)b * p.H + h) * p.T + t) * kHeadDim + 8 * c) = w[u];
+        } else if (h < Hkv) {
+            if (p.k_out) *reinterpret_cast<uint4*>(p.k_out + (((long long)b * Hkv + h) * p.T + t) * kHeadDim + 8 * c) = w[u];
+            if (paged)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kv.k) + page * p.kv.k_stride_page +
+                                          slot * p.kv.k_stride_slot + h * p.kv.k_stride_head + 8 * c) = w[u];
+        } else if (paged) {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.kv.v) + page * p.kv.v_stride_page +
+                                      slot * p.kv.v_stride_slot + (h - Hkv) * p.kv.v_stride_head + 8 * c) = w[u];
+        }
     }
-    if (isk && p.k_out)
-        *reinterpret_cast<uint4*>(p.k_out + (((int64_t)b * p.kv.H_kv + h) * p.T + t) * kHeadDim + 8 * c) = w;
-    const int page = p.page_table[(int64_t)b * p.max_pages + pos / p.kv.page_size];
-    if (page < 0 || page >= p.kv.num_pages) return;
-    const int slot = (int)(pos % p.kv.page_size);
-    __nv_bfloat16* dst =
-        isk ? static_cast<__nv_bfloat16*>(p.kv.k) + page * p.kv.k_stride_page + h * p.kv.k_stride_head + slot * p.kv.k_stride_slot
-            : static_cast<__nv_bfloat16*>(p.kv.v) + page * p.kv.v_stride_page + h * p.kv.v_stride_head + slot * p.kv.v_stride_slot;
-    *reinterpret_cast<uint4*>(dst + 8 * c) = w;
+}
+
+template <int U>
+cudaError_t launch(AppendParams& p, cudaStream_t stream) {
+    p.units = (p.H + 2 * p.kv.H_kv + U - 1) / U;
+    p.by_units = divisor(p.units);
+    const int64_t units = ((int64_t)p.B * p.T + 7) / 8 * p.units;  // four to a block
+    launch_begin(KID_KV_APPEND, stream);
+    kv_append_kernel<U><<<(unsigned)((units + 3) / 4), 256, 0, stream>>>(p);
+    launch_end(KID_KV_APPEND, stream);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -131,12 +140,12 @@ cudaError_t launch_rope_table(float* table, int max_pos, int rot_dim, double bas
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
-    const int64_t threads = (int64_t)p.B * p.T * (p.H + 2 * p.kv.H_kv) * 8;
-    launch_begin(KID_KV_APPEND, stream);
-    kv_append_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(p);
-    launch_end(KID_KV_APPEND, stream);
-    return cudaGetLastError();
+cudaError_t launch_kv_append(AppendParams& p, cudaStream_t stream) {
+    p.by_T = divisor(p.T);
+    p.log_page = 0;
+    while ((1 << p.log_page) < p.kv.page_size) ++p.log_page;
+    // few rows: one per eight lanes, for the most of them at once
+    return (int64_t)p.B * p.T * (p.H + 2 * p.kv.H_kv) < 16384 ? launch<1>(p, stream) : launch<4>(p, stream);
 }
 
 }  // namespace saf

@@ -20,6 +20,20 @@ struct HeadBits {
     __host__ __device__ bool get(int h) const { return (w[h >> 5] >> (h & 31)) & 1u; }
 };
 
+// Division by a launch constant: n / d = (umulhi(n, m) + n) >> s for 0 <= n < 2^31, with 2^(s-1) < d <= 2^s and
+// m = floor(2^32 (2^s - d) / d) + 1 (the round-up method of Granlund and Montgomery).  A few cycles, where the
+// general division's code, cold at the start of a launch, costs hundreds.
+struct Divisor {
+    uint32_t m, s;
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+};
+inline Divisor divisor(int d) {
+    Divisor x{0, 0};
+    while ((1ll << x.s) < d) ++x.s;
+    x.m = (uint32_t)(((1ull << 32) * ((1ull << x.s) - (uint64_t)d)) / (uint64_t)d + 1);
+    return x;
+}
+
 // What the append kernel needs, by value.
 struct AppendParams {
     saf_paged_kv kv;
@@ -32,6 +46,8 @@ struct AppendParams {
     HeadBits keyless;    // per K/V head: all its query heads are replaced
     const int32_t *page_table, *seq_lens, *q_lens;
     int max_pages, B, H, T, max_len;
+    int units, log_page;       // groups of rows per token
+    Divisor by_units, by_T;
 };
 
 // A paged attention call (checked by the ABI layer).
@@ -60,20 +76,6 @@ struct RowInfo {
     int out, part;  // its row of the output (-1: it has no token), and of the prefix's parts
     int replaced;   // its head + 1, or 0
 };
-
-// Division by a launch constant: n / d = (umulhi(n, m) + n) >> s for 0 <= n < 2^31, with 2^(s-1) < d <= 2^s and
-// m = floor(2^32 (2^s - d) / d) + 1 (the round-up method of Granlund and Montgomery).  A few cycles, where the
-// general division's code, cold at the start of a launch, costs hundreds.
-struct Divisor {
-    uint32_t m, s;
-    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
-};
-inline Divisor divisor(int d) {
-    Divisor x{0, 0};
-    while ((1ll << x.s) < d) ++x.s;
-    x.m = (uint32_t)(((1ull << 32) * ((1ull << x.s) - (uint64_t)d)) / (uint64_t)d + 1);
-    return x;
-}
 
 // A row's (m, l, O) before the division, of a block of rows: [rows][64] O, then m, then l.
 struct RowsRef {
@@ -398,7 +400,7 @@ cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix,
 
 size_t paged_workspace_bytes(int B, int H, int H_kv, int T, int prefix_len);
 cudaError_t launch_rope_table(float* table, int max_pos, int rot_dim, double base, cudaStream_t stream);
-cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_append(AppendParams& p, cudaStream_t stream);
 cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream);
 
 }  // namespace saf

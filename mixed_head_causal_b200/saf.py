@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -427,18 +428,18 @@ def rope_table(max_pos: int, rot_dim: int = HEAD_DIM, base: float = 10000.0, dev
     return table
 
 
-_Strides = ctypes.c_int64 * 3
+_pack_strides = struct.Struct("3q").pack
 
 
-def _strided(name: str, t: torch.Tensor, shape, device):
-    """The (batch, head, token) strides of a bf16 tensor of this shape, for the library."""
+def _strided(name: str, t: torch.Tensor, shape, device) -> bytes:
+    """The (batch, head, token) strides of a bf16 tensor of this shape, as the library reads them."""
     st = t.stride()
     if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device or st[3] != 1:
         raise ValueError(f"{name}: expected bf16 of shape {tuple(shape)} with a contiguous last axis on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
     if (st[0] | st[1] | st[2]) & 7:     # the stride of an axis of one entry is never used, and may be odd
         st = [0 if n <= 1 else x for x, n in zip(st, shape)]
-    return _Strides(st[0], st[1], st[2])
+    return _pack_strides(st[0], st[1], st[2])
 
 
 @_annotated
