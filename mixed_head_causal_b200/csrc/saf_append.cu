@@ -42,6 +42,8 @@ __device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t y, uint64_t cs, ui
 // head are then written 1 KB at a stretch.
 template <int U>
 __global__ void __launch_bounds__(256, U == 1 ? 6 : 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    tc::griddep_wait();  // (the launch may overlap the one before it on the stream)
+    tc::griddep_launch_dependents();
     const int unit = blockIdx.x * 4 + (threadIdx.x >> 6), c = threadIdx.x & 7;
     const int tok8 = p.by_units.div(unit), r0 = (unit - tok8 * p.units) * U;
     const int tok = tok8 * 8 + ((threadIdx.x >> 3) & 7);
@@ -125,9 +127,18 @@ cudaError_t launch(AppendParams& p, cudaStream_t stream) {
     p.by_units = divisor(p.units);
     const int64_t units = ((int64_t)p.B * p.T + 7) / 8 * p.units;  // four to a block
     launch_begin(KID_KV_APPEND, stream);
-    kv_append_kernel<U><<<(unsigned)((units + 3) / 4), 256, 0, stream>>>(p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((units + 3) / 4));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_append_kernel<U>, p);
     launch_end(KID_KV_APPEND, stream);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

@@ -124,8 +124,11 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
+    // The launch may overlap the one before it on the stream, whose results are awaited before any is read.  After a
+    // prefix's launch, which has waited for what came before both, only its results are (see below).
+    if (PREFIX || !p.prefix.part) griddep_wait();
+    griddep_launch_dependents();
     __syncthreads();
-    if (PREFIX) griddep_launch_dependents();  // the batch's own keys may start
 
     if (warp == NCW) {
         // ------------------------------------------------ producer
@@ -306,13 +309,25 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 mine[first * RED_PITCH + lane] = ahead[0] + ahead[2];
                 mine[first * RED_PITCH + lane + 32] = ahead[1] + ahead[3];
                 load_ahead(k0 - turns * tk);
-                for (uint32_t left = x.replaced & (x.replaced - 1); left; left &= left - 1) {
-                    const int row = __ffs(left) - 1;
-                    const RowInfo& w = info[row];
+                for (uint32_t left = x.replaced & (x.replaced - 1); left;) {  // four rows' loads at a time
+                    float v[4][4];
+                    int rows[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = min(k0 + lane + 32 * e, w.vis - 1);
-                        mine[row * RED_PITCH + lane + 32 * e] = __ldg(p.a + w.a0 + j) + __ldg(p.r + w.r0 - j);
+                    for (int u = 0; u < 4; ++u) {
+                        rows[u] = left ? __ffs(left) - 1 : rows[0];
+                        left &= left - 1;
+                        const RowInfo& w = info[rows[u]];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = min(k0 + lane + 32 * e, w.vis - 1);
+                            v[u][e] = __ldg(p.a + w.a0 + j);
+                            v[u][2 + e] = __ldg(p.r + w.r0 - j);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        mine[rows[u] * RED_PITCH + lane] = v[u][0] + v[u][2];
+                        mine[rows[u] * RED_PITCH + lane + 32] = v[u][1] + v[u][3];
                     }
                 }
                 __syncwarp();
@@ -592,8 +607,7 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
 }
 
 template <int NB, bool PREFIX>
-cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const PagedParams& p, bool overlap,
-                         cudaStream_t stream) {
+cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const PagedParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<NB, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem<NB>::TOTAL);
     if (e != cudaSuccess) return e;
@@ -606,7 +620,7 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cfg.numAttrs = 1;
     const int kid = PREFIX ? KID_PAGED_PREFIX : KID_PAGED_ATTN;
     launch_begin(kid, stream);
     e = cudaLaunchKernelEx(&cfg, paged_split_kernel<NB, PREFIX>, mk, mv, p);
@@ -616,8 +630,7 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
 }
 
 template <bool PREFIX>
-cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, bool overlap,
-                              cudaStream_t stream) {
+cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, cudaStream_t stream) {
     const int per = block_rows(p.rows);
     p.nrb = (p.rows + per - 1) / per;
     p.by_T = divisor(p.T);
@@ -625,10 +638,10 @@ cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, Page
     p.by_nrb = divisor(p.nrb);
     if (!axis_fits<SplitAxis>(p)) return cudaErrorNotSupported;
     switch (per / 8) {
-        case 1: return launch_split<1, PREFIX>(mk, mv, p, overlap, stream);
-        case 2: return launch_split<2, PREFIX>(mk, mv, p, overlap, stream);
-        case 3: return launch_split<3, PREFIX>(mk, mv, p, overlap, stream);
-        default: return launch_split<4, PREFIX>(mk, mv, p, overlap, stream);
+        case 1: return launch_split<1, PREFIX>(mk, mv, p, stream);
+        case 2: return launch_split<2, PREFIX>(mk, mv, p, stream);
+        case 3: return launch_split<3, PREFIX>(mk, mv, p, stream);
+        default: return launch_split<4, PREFIX>(mk, mv, p, stream);
     }
 }
 
@@ -682,8 +695,8 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
         p.rows = c.B * p.R;
         p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[1]);
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
-        const cudaError_t e = p.rows > kTcRows ? launch_paged_tc(c.kv, p, true, false, stream)
-                                               : launch_split_rows<true>(mk, mv, p, false, stream);
+        const cudaError_t e = p.rows > kTcRows ? launch_paged_tc(c.kv, p, true, stream)
+                                               : launch_split_rows<true>(mk, mv, p, stream);
         if (e != cudaSuccess) return e;
     }
     p.table = c.page_table;
@@ -692,8 +705,8 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.rows = p.R;
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
-    if (p.rows <= kTcRows) return launch_split_rows<false>(mk, mv, p, c.prefix_len > 0, stream);
-    return launch_paged_tc(c.kv, p, false, c.prefix_len > 0, stream);
+    if (p.rows <= kTcRows) return launch_split_rows<false>(mk, mv, p, stream);
+    return launch_paged_tc(c.kv, p, false, stream);
 }
 
 }  // namespace saf

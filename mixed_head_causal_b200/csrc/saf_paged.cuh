@@ -396,7 +396,7 @@ bool axis_fits(const PagedParams& p) {
 constexpr int kMaxGrid = 320;
 inline int paged_grid() { return std::min(kMaxGrid, 2 * sm_count()); }
 // The tensor-core kernel (saf_paged_tc.cu): items of up to 128 rows.
-cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, bool overlap, cudaStream_t stream);
+cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, cudaStream_t stream);
 
 size_t paged_workspace_bytes(int B, int H, int H_kv, int T, int prefix_len);
 cudaError_t launch_rope_table(float* table, int max_pos, int rot_dim, double base, cudaStream_t stream);

@@ -535,7 +535,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         tmem_alloc(smem_addr(tmem_holder), TMEM_COLS);
         tmem_relinquish();
     }
-    if (PREFIX) griddep_launch_dependents();  // the batch's own keys may start
+    // The launch may overlap the one before it on the stream, whose results are awaited before any is read.  After a
+    // prefix's launch, which has waited for what came before both, only its results are (see below).
+    if (PREFIX || !p.prefix.part) griddep_wait();
+    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -839,7 +842,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 }
 
 template <bool PREFIX>
-cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStream_t stream) {
+cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) {
     CUtensorMap mk, mv;
     if (!make_tmap_pages(kv, true, BN, &mk) || !make_tmap_pages(kv, false, BN, &mv)) return cudaErrorNotSupported;
     p.nrb = (p.rows + BM - 1) / BM;
@@ -874,7 +877,7 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStr
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cfg.numAttrs = 1;
     const int kid = PREFIX ? KID_PAGED_PREFIX_TC : KID_PAGED_TC;
     launch_begin(kid, stream);
     e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<PREFIX>, mk, mv, p);
@@ -885,8 +888,8 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, bool overlap, cudaStr
 
 }  // namespace
 
-cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, bool overlap, cudaStream_t stream) {
-    return prefix ? launch<true>(kv, p, overlap, stream) : launch<false>(kv, p, overlap, stream);
+cudaError_t launch_paged_tc(const saf_paged_kv& kv, PagedParams& p, bool prefix, cudaStream_t stream) {
+    return prefix ? launch<true>(kv, p, stream) : launch<false>(kv, p, stream);
 }
 
 }  // namespace saf
