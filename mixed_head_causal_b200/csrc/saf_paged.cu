@@ -126,7 +126,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     }
     // The launch may overlap the one before it on the stream, whose results are awaited before any is read.  After a
     // prefix's launch, which has waited for what came before both, only its results are (see below).
-    if (PREFIX || !p.prefix.part) griddep_wait();
+    if (PREFIX || !p.part) griddep_wait();
     griddep_launch_dependents();
     __syncthreads();
 
@@ -511,7 +511,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
         join_warps();
         const int c = (tid & 15) * 4;
-        if (!PREFIX && p.prefix.part && !waited) {
+        if (!PREFIX && p.part && !waited) {
             griddep_wait();
             waited = true;
         }
@@ -687,8 +687,8 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
                 if (c.replaced.get(h) == (want == 1)) p.heads[at++] = (uint8_t)h;
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
-        p.prefix.part = reinterpret_cast<float*>(c.ws + w.part);
-        p.prefix.nrows = c.B * c.H * c.T;
+        p.part = reinterpret_cast<float*>(c.ws + w.part);
+        p.part_rows = c.B * c.H * c.T;
         p.table = c.prefix_table;
         p.table_stride = 0;
         p.nseq = 1;

@@ -12,7 +12,7 @@ namespace saf {
 
 // Kernel ids of the launch accounting, after those of saf_common.cuh.
 constexpr int KID_ROPE_TABLE = 15, KID_KV_APPEND = 16, KID_PAGED_ATTN = 17, KID_PAGED_PREFIX = 18, KID_PAGED_TC = 19,
-              KID_PAGED_PREFIX_TC = 20;
+              KID_PAGED_PREFIX_TC = 20, KID_PAGED_JOIN = 21;
 
 // Head kinds by value: bit h set = head h is one.
 struct HeadBits {
@@ -77,25 +77,6 @@ struct RowInfo {
     int replaced;   // its head + 1, or 0
 };
 
-// A row's (m, l, O) before the division, of a block of rows: [rows][64] O, then m, then l.
-struct RowsRef {
-    const float *o, *m, *l;
-};
-// What the prefix came to, for the kernel of the batch's own keys: rows in the
-// order K/V head (by order[]), head of the group, sequence, token.  Rows of an item
-// that one CTA held whole are in `part` (all rows); the tensor-core kernel leaves
-// the others' in its CTAs' slots, to be joined where they are wanted (pieces of one
-// item by one CTA: 50 us for 16 items of 18 pieces).  part null: no prefix.
-struct PrefixParts {
-    float* part;
-    int nrows;          // all rows
-    const float* slots;  // null: everything is in `part`
-    int slot_floats;
-    int per, more, units, tiles, item_units, snap, nrb;  // the launch's axis, see AxisWalk
-    Divisor by_rows;    // rows of a K/V head
-    int rows;
-};
-
 // What the attention kernels need, by value.
 struct PagedParams {
     const __nv_bfloat16* q;
@@ -114,7 +95,10 @@ struct PagedParams {
     uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
-    PrefixParts prefix;
+    // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order K/V
+    // head (by order[]), head of the group, sequence, token.
+    float* part;
+    int part_rows;
 };
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int code) {
@@ -188,35 +172,13 @@ __device__ __forceinline__ int pieces_of(int per, int more, int item_units, int 
     return c2 - c1 + 1;
 }
 // Four columns of a row (from c) joined with what the prefix came to: o, m and l are updated.
-__device__ __forceinline__ void join_prefix(const PagedParams& p, int row, int c, float4& o, float& m, float& l) {
-    const PrefixParts& x = p.prefix;
-    int pieces = 1, c_first = 0, in_block = 0;
-    if (x.slots) {
-        const int gi = x.by_rows.div(row), rr = row - gi * x.rows;
-        in_block = rr & 127;
-        pieces = pieces_of(x.per, x.more, x.item_units, x.snap, (gi * x.nrb + (rr >> 7)) * x.units, x.tiles, c_first);
-    }
-    auto part = [&](int k) {
-        if (pieces == 1)
-            return RowsRef{x.part + (size_t)row * kHeadDim, x.part + (size_t)x.nrows * kHeadDim + row,
-                           x.part + (size_t)x.nrows * (kHeadDim + 1) + row};
-        const float* sl = x.slots + ((size_t)(c_first + k) * 2 + (k == 0)) * x.slot_floats;
-        return RowsRef{sl + in_block * kHeadDim, sl + 128 * kHeadDim + in_block, sl + 128 * (kHeadDim + 1) + in_block};
-    };
-    float mm = m;
-#pragma unroll 8
-    for (int k = 0; k < pieces; ++k) mm = fmaxf(mm, __ldcg(part(k).m));
-    const float f = weight(m, mm);
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    l *= f;
-#pragma unroll 8
-    for (int k = 0; k < pieces; ++k) {
-        const RowsRef r = part(k);
-        const float fk = weight(__ldcg(r.m), mm);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(r.o + c));
-        o = make_float4(o.x + fk * v.x, o.y + fk * v.y, o.z + fk * v.z, o.w + fk * v.w);
-        l += fk * __ldcg(r.l);
-    }
+__device__ __forceinline__ void join_part(const PagedParams& p, int row, int c, float4& o, float& m, float& l) {
+    const float* ml = p.part + (size_t)p.part_rows * kHeadDim + row;
+    const float4 o2 = __ldcg(reinterpret_cast<const float4*>(p.part + (size_t)row * kHeadDim + c));
+    const float m2 = __ldcg(ml), l2 = __ldcg(ml + p.part_rows);
+    const float mm = fmaxf(m, m2), f = weight(m, mm), f2 = weight(m2, mm);
+    o = make_float4(o.x * f + o2.x * f2, o.y * f + o2.y * f2, o.z * f + o2.z * f2, o.w * f + o2.w * f2);
+    l = l * f + l2 * f2;
     m = mm;
 }
 // A finished row (four columns from c) to the output.
@@ -233,14 +195,13 @@ template <bool PREFIX>
 __device__ __forceinline__ void finish_row(const PagedParams& p, const RowInfo& x, int c, float4 o, float m, float l) {
     if (x.out < 0) return;
     if (PREFIX) {
-        float* part = p.prefix.part;
-        *reinterpret_cast<float4*>(part + (size_t)x.part * kHeadDim + c) = o;
+        *reinterpret_cast<float4*>(p.part + (size_t)x.part * kHeadDim + c) = o;
         if (c == 0) {
-            part[(size_t)p.prefix.nrows * kHeadDim + x.part] = m;
-            part[(size_t)p.prefix.nrows * (kHeadDim + 1) + x.part] = l;
+            p.part[(size_t)p.part_rows * kHeadDim + x.part] = m;
+            p.part[(size_t)p.part_rows * (kHeadDim + 1) + x.part] = l;
         }
     } else {
-        if (p.prefix.part) join_prefix(p, x.part, c, o, m, l);
+        if (p.part) join_part(p, x.part, c, o, m, l);
         store_row(p, x, c, o, m, l);
     }
 }

@@ -7,7 +7,9 @@
 // where it ends).  The blocks of all items form one axis, of which every CTA of two
 // per SM takes an equal stretch, as in the kernel for few rows (saf_paged.cu).  An
 // item that several share is joined by the CTA that finishes its last piece, in
-// key order, or with a prefix by those who want its rows.  Six warps:
+// key order, or with a prefix, whose few items are cut into many pieces, by a
+// launch of its own with a thread per four columns of every row (one CTA took 50 us
+// over 18 pieces of 128 rows).  Six warps:
 //   warp 0      producer: walks the stretch, page look-up and TMA loads, a box per
 //               page, two stages each of K and V (no K where all rows are replaced)
 //   warp 1      TMEM owner and MMA issuer (one elected lane):
@@ -537,7 +539,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     // The launch may overlap the one before it on the stream, whose results are awaited before any is read.  After a
     // prefix's launch, which has waited for what came before both, only its results are (see below).
-    if (PREFIX || !p.prefix.part) griddep_wait();
+    if (PREFIX || !p.part) griddep_wait();
     griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -764,7 +766,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (ok && x.nt > 0) ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
             tc_fence_after();
             if (!ok) break;
-            if (!PREFIX && p.prefix.part && !waited) {
+            if (!PREFIX && p.part && !waited) {
                 griddep_wait();
                 waited = true;
             }
@@ -794,7 +796,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 __stcg(slot + BM * kHeadDim + row, m);
                 __stcg(slot + BM * (kHeadDim + 1) + row, l);
             }
-            if (!PREFIX && x.pieces > 1) {  // (a prefix's pieces are joined where they are wanted)
+            if (!PREFIX && x.pieces > 1) {
                 __threadfence();
                 join_warps();
                 if (row == 0) *last_flag = atomicAdd(p.counters + x.c_first, 1u) == (unsigned)x.pieces - 1;
@@ -841,6 +843,46 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
 }
 
+// Joins the pieces of a prefix's items that several CTAs shared: sixteen threads per
+// row.  There is one sequence, of known length, so that the axis is the host's too.
+struct JoinParams {
+    const float* slots;
+    float* part;
+    int rows, part_rows, nrb, tiles, per, more;  // rows of a K/V head
+    Divisor by_rows;
+};
+__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinParams p) {
+    griddep_launch_dependents();  // (what comes after reads nothing of this call's before it waits in turn)
+    griddep_wait();
+    constexpr int SLOT = BM * (kHeadDim + 2);
+    const int row = blockIdx.x * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    if (row >= p.part_rows) return;
+    const int gi = p.by_rows.div(row), rr = row - gi * p.rows, in_block = rr & (BM - 1);
+    int first;
+    const int pieces = pieces_of(p.per, p.more, TcAxis::kItem, TcAxis::kSnap,
+                                 (gi * p.nrb + rr / BM) * (p.tiles + TcAxis::kItem), p.tiles, first);
+    if (pieces == 1) return;
+    auto slot_of = [&](int k) { return p.slots + ((size_t)(first + k) * 2 + (k == 0)) * SLOT; };
+    float mm = kNegInf;
+#pragma unroll 8
+    for (int k = 0; k < pieces; ++k) mm = fmaxf(mm, slot_of(k)[BM * kHeadDim + in_block]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < pieces; ++k) {
+        const float* sl = slot_of(k);
+        const float f = weight(sl[BM * kHeadDim + in_block], mm);
+        const float4 v = *reinterpret_cast<const float4*>(sl + in_block * kHeadDim + c);
+        o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
+        l += f * sl[BM * (kHeadDim + 1) + in_block];
+    }
+    *reinterpret_cast<float4*>(p.part + (size_t)row * kHeadDim + c) = o;
+    if (c == 0) {
+        p.part[(size_t)p.part_rows * kHeadDim + row] = mm;
+        p.part[(size_t)p.part_rows * (kHeadDim + 1) + row] = l;
+    }
+}
+
 template <bool PREFIX>
 cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) {
     CUtensorMap mk, mv;
@@ -850,21 +892,6 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) 
     p.by_BT = divisor(p.B * p.T);
     p.by_nrb = divisor(p.nrb);
     if (!axis_fits<TcAxis>(p)) return cudaErrorNotSupported;
-    if (PREFIX) {  // for those that join it: AxisWalk's own figures, there being one sequence of known length
-        PrefixParts& x = p.prefix;
-        x.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
-        x.units = x.tiles + TcAxis::kItem;
-        x.item_units = TcAxis::kItem;
-        x.snap = TcAxis::kSnap;
-        x.nrb = p.nrb;
-        x.rows = p.rows;
-        x.by_rows = divisor(p.rows);
-        const int total = p.Hkv * p.nrb * x.units, ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
-        x.per = total / ctas;
-        x.more = total - x.per * ctas;
-        x.slots = p.slots;
-        x.slot_floats = BM * (kHeadDim + 2);
-    }
     const int smem = SM_TOTAL;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -882,8 +909,26 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) 
     launch_begin(kid, stream);
     e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<PREFIX>, mk, mv, p);
     launch_end(kid, stream);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    if (e != cudaSuccess || !PREFIX) return e != cudaSuccess ? e : cudaGetLastError();
+    JoinParams j;  // AxisWalk's own figures
+    j.slots = p.slots;
+    j.part = p.part;
+    j.rows = p.rows;
+    j.part_rows = p.part_rows;
+    j.nrb = p.nrb;
+    j.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
+    j.by_rows = divisor(p.rows);
+    const int total = p.Hkv * p.nrb * (j.tiles + TcAxis::kItem);
+    const int ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
+    j.per = total / ctas;
+    j.more = total - j.per * ctas;
+    cfg.gridDim = dim3((unsigned)((p.part_rows + 15) / 16));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    launch_begin(KID_PAGED_JOIN, stream);
+    e = cudaLaunchKernelEx(&cfg, prefix_join_kernel, j);
+    launch_end(KID_PAGED_JOIN, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

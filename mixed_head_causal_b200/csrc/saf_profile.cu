@@ -24,7 +24,7 @@ struct Profile {
 
 const char* kNames[] = {"?", "pattern", "fwd_mma", "dot", "dkdv_mma", "dq_mma",
                         "fwd_tc", "bwd_tc", "(retired)", "dq_convert", "bwd_pre", "group_sum", "pattern_grad", "calibration", "fit",
-                        "rope_table", "kv_append", "paged_attn", "paged_prefix", "paged_tc", "paged_prefix_tc"};
+                        "rope_table", "kv_append", "paged_attn", "paged_prefix", "paged_tc", "paged_prefix_tc", "paged_join"};
 
 void release_locked() {
     for (auto& r : g_prof.recs) {
