@@ -44,7 +44,7 @@ using mma::mma_bf16;
 constexpr int TK = 64;               // keys per tile with K and V (twice as many of V alone)
 constexpr int CTAS_PER_SM = 2;
 struct SplitAxis {
-    static constexpr int kTile = TK, kTileKeyless = 2 * TK, kItem = 4, kSnap = 4, kMinUnits = 8;
+    static constexpr int kTile = TK, kTileKeyless = 2 * TK, kUnit = 1, kUnitKeyless = 1, kItem = 4, kSnap = 4, kMinUnits = 8;
 };
 constexpr int kMaxBlocks = 4;        // row blocks of eight that one item holds
 constexpr uint32_t HALF = TK * 128;  // bytes of a tile's K or V
@@ -167,12 +167,11 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
                 return;
             }
-            const int g = p.order[w.gi], row0 = w.rb * ROWS;
-            x.rows = min(ROWS, p.rows - row0);
+            const int g = p.e_g[w.e], row0 = w.rb * ROWS;
+            x.rows = min(ROWS, max(0, p.e_heads[w.e] * w.n_rows - row0));
             int out;
             {  // a lane per row
-                const int n = PREFIX ? 0 : new_tokens(p, w.b);
-                const RowInfo row = row_info<PREFIX>(p, w.b, w.gi, w.len, n, p.prefix_len + w.len - n, row0 + lane);
+                const RowInfo row = row_info<PREFIX>(p, w.b, w.e, w.len, w.n_rows, row0 + lane);
                 x.replaced = __ballot_sync(~0u, lane < x.rows && row.replaced && row.vis > 0);
                 x.vmin = __reduce_min_sync(~0u, lane < x.rows && row.out >= 0 ? row.vis : INT_MAX);
                 out = row.out;
@@ -631,13 +630,11 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
 
 template <bool PREFIX>
 cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, cudaStream_t stream) {
-    const int per = block_rows(p.rows);
-    p.nrb = (p.rows + per - 1) / per;
-    p.by_T = divisor(p.T);
-    p.by_BT = divisor(p.B * p.T);
-    p.by_nrb = divisor(p.nrb);
-    if (!axis_fits<SplitAxis>(p)) return cudaErrorNotSupported;
-    switch (per / 8) {
+    make_entries(p, p.G, false);
+    p.block_rows = block_rows(PREFIX ? p.B * p.R : p.R);
+    p.by_block = divisor(p.block_rows);
+    if (!axis_fits<SplitAxis>(p, PREFIX)) return cudaErrorNotSupported;
+    switch (p.block_rows / 8) {
         case 1: return launch_split<1, PREFIX>(mk, mv, p, stream);
         case 2: return launch_split<2, PREFIX>(mk, mv, p, stream);
         case 3: return launch_split<3, PREFIX>(mk, mv, p, stream);
@@ -675,16 +672,12 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.G = c.H / c.kv.H_kv;
     p.R = p.G * c.T;
     p.max_len = c.max_len;
-    int n = 0;
-    for (int want = 0; want < 2; ++want) {  // those with keys, then those without
-        for (int g = 0; g < p.Hkv; ++g)
-            if (c.keyless.get(g) == (want == 1)) p.order[n++] = (uint8_t)g;
-        if (want == 0) p.keyed = n;
-    }
     for (int g = 0, at = 0; g < p.Hkv; ++g)
         for (int want = 0; want < 2; ++want)
             for (int h = g * p.G; h < (g + 1) * p.G; ++h)
                 if (c.replaced.get(h) == (want == 1)) p.heads[at++] = (uint8_t)h;
+    p.by_T = divisor(p.T);
+    p.by_BT = divisor(p.B * p.T);
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
         p.part = reinterpret_cast<float*>(c.ws + w.part);
@@ -692,20 +685,18 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
         p.table = c.prefix_table;
         p.table_stride = 0;
         p.nseq = 1;
-        p.rows = c.B * p.R;
         p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[1]);
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
-        const cudaError_t e = p.rows > kTcRows ? launch_paged_tc(c.kv, p, true, stream)
+        const cudaError_t e = c.B * p.R > kTcRows ? launch_paged_tc(c.kv, p, true, stream)
                                                : launch_split_rows<true>(mk, mv, p, stream);
         if (e != cudaSuccess) return e;
     }
     p.table = c.page_table;
     p.table_stride = c.max_pages;
     p.nseq = c.B;
-    p.rows = p.R;
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
-    if (p.rows <= kTcRows) return launch_split_rows<false>(mk, mv, p, stream);
+    if (p.R <= kTcRows) return launch_split_rows<false>(mk, mv, p, stream);
     return launch_paged_tc(c.kv, p, false, stream);
 }
 

@@ -88,11 +88,14 @@ struct PagedParams {
     const int32_t *table, *seq_lens, *q_lens;
     int table_stride, num_pages, log_page, Hkv;
     int B, H, T, G, R, max_len;  // R = G T rows of one (b, g)
-    int nseq, rows, nrb;         // key sequences, rows of one item list entry, row blocks
-    Divisor by_T, by_BT, by_nrb;
-    int keyed;                   // K/V heads with keys: the first of order[]
-    uint8_t order[kMaxHeads];    // K/V heads, those with keys first
+    int nseq;                    // key sequences (1 for the prefix)
+    // The rows that share keys and an item list: entry e holds e_heads[e] of K/V head e_g[e]'s query heads, from
+    // heads[e_g[e] * G + e_first[e]] on, hp at most.  The keyed ones come first; the others' rows are all replaced.
+    int entries, keyed, hp, block_rows;
+    uint8_t e_g[kMaxHeads], e_first[kMaxHeads];
+    uint16_t e_heads[kMaxHeads];
     uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
+    Divisor by_T, by_BT, by_block;
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
     // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order K/V
@@ -124,33 +127,38 @@ __device__ __forceinline__ int key_len(const PagedParams& p, int b) {
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
     return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
 }
-// Row rr of the item list entry (b, K/V head order[gi]), head by head (the ordinary heads of the
-// group first): with PREFIX (head, sequence, token), else (head, token) of sequence b.  n, pos0: the
-// sequence's new tokens and the position of the first (with PREFIX they are
-// looked up per row).
+// Tokens of a head of a sequence's entries: with PREFIX those of the whole batch,
+// else the sequence's new ones.
 template <bool PREFIX>
-__device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int gi, int len, int n, int pos0, int rr) {
+__device__ __forceinline__ int head_rows(const PagedParams& p, int b) {
+    return PREFIX ? p.B * p.T : new_tokens(p, b);
+}
+// Row rr of entry e of sequence b, head by head: with PREFIX (head, sequence,
+// token), else (head, token).  len: keys; n: head_rows.
+template <bool PREFIX>
+__device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int e, int len, int n, int rr) {
     RowInfo x;
     x.a0 = x.r0 = 0;
     x.vis = x.part = 0;
     x.out = -1;
     x.replaced = 0;
-    if (rr >= p.rows) return x;
-    const int u = (PREFIX ? p.by_BT : p.by_T).div(rr), h = p.heads[p.order[gi] * p.G + u];
-    const int rem = rr - u * (PREFIX ? p.B * p.T : p.T);
+    if (rr >= p.e_heads[e] * n) return x;
+    const int u = PREFIX ? p.by_BT.div(rr) : n == 1 ? rr : (int)((unsigned)rr / (unsigned)n), rem = rr - u * n;
     const int rb = PREFIX ? p.by_T.div(rem) : b, t = PREFIX ? rem - rb * p.T : rem;
+    const int hs = p.e_g[e] * p.G + p.e_first[e] + u, h = p.heads[hs];
+    int pos = p.prefix_len + len - n + t;
     if (PREFIX) {
-        n = new_tokens(p, rb);
-        pos0 = p.prefix_len + key_len<false>(p, rb) - n;
+        const int n_new = new_tokens(p, rb);
+        if (t >= n_new) return x;
+        pos = p.prefix_len + key_len<false>(p, rb) - n_new + t;
     }
-    if (t >= n) return x;
     const int key_base = PREFIX ? 0 : p.prefix_len;  // position of local key 0
     const long long ph = (long long)h * p.pattern_len;
-    x.vis = max(0, min(len, pos0 + t - key_base + 1));
+    x.vis = max(0, min(len, pos - key_base + 1));
     x.a0 = ph + key_base;
-    x.r0 = ph + pos0 + t - key_base;
+    x.r0 = ph + pos - key_base;
     x.out = (rb * p.H + h) * p.T + t;
-    x.part = ((gi * p.G + u) * p.B + rb) * p.T + t;
+    x.part = (hs * p.B + rb) * p.T + t;
     x.replaced = p.replaced.get(h) ? h + 1 : 0;
     return x;
 }
@@ -164,9 +172,9 @@ __device__ __forceinline__ int first_from(int per, int more, int x) {
 }
 // The CTAs that share the item that begins at unit `start`: how many, and the
 // first (where there are several).
-__device__ __forceinline__ int pieces_of(int per, int more, int item_units, int snap, int start, int tiles, int& c_first) {
+__device__ __forceinline__ int pieces_of(int per, int more, int item_units, int snap, int start, int tile_units, int& c_first) {
     // the stretches that begin strictly inside the item, by more than a snap
-    const int in_lo = start + item_units + snap + 1, in_hi = start + item_units + tiles - snap;
+    const int in_lo = start + item_units + snap + 1, in_hi = start + item_units + tile_units - snap;
     const int c1 = in_lo < in_hi ? first_from(per, more, in_lo) : 0, c2 = in_lo < in_hi ? first_from(per, more, in_hi) : 0;
     c_first = c1 - 1;
     return c2 - c1 + 1;
@@ -207,33 +215,41 @@ __device__ __forceinline__ void finish_row(const PagedParams& p, const RowInfo& 
 }
 
 // ---------------------------------------------------------------- the axis of tiles
-// Items (sequence b, K/V head, row block) one after the other, each kItem units
-// that stand for no tile (its own cost) and one per tile; every CTA takes an equal
-// stretch, moved to an item's end where it would end within kSnap units of one.
-// A: tile sizes (keys) of K/V heads with and without keys, and these constants.
+// Items (sequence b, entry, row block) one after the other, each kItem units that
+// stand for no tile (its own cost) and kUnit or kUnitKeyless per tile; every CTA
+// takes an equal stretch, moved to an item's end where it would end within kSnap
+// units of one.  A: these constants, and the tile sizes (keys) of entries with and
+// without keys.
 struct Stretch {
-    int b, gi, rb, len, n;  // item; its keys and tiles (one without keys still takes one, empty, tile: its rows are written)
+    int b, e, rb, len, n_rows, n;  // item; its sequence's keys and head_rows; its tiles (one without keys still takes one,
+                                   // empty, tile: its rows are written)
     bool keyed;
-    int t0, t1;             // this CTA's tiles of it
-    int pieces, c_first;    // CTAs that share it, and the first of them
+    int t0, t1;                    // this CTA's tiles of it
+    int pieces, c_first;           // CTAs that share it, and the first of them
 };
 template <class A, bool PREFIX>
 struct AxisWalk {
     const PagedParams& p;
-    int total, ctas, per, more;  // units; stretch c begins at c * per + min(c, more)
-    int u, end, b, base, len;    // next unit, end of the stretch, current sequence and its first unit
+    int total, ctas, per, more;    // units; stretch c begins at c * per + min(c, more)
+    int u, end, b, base, len, nr;  // next unit, end of the stretch, current sequence: first unit, keys, head_rows
     __device__ __forceinline__ static int tiles_of(int len, bool keyed) {
         const int tk = keyed ? A::kTile : A::kTileKeyless;
         return max(1, (len + tk - 1) / tk);
     }
-    __device__ __forceinline__ int seq_units(int n) const {
-        return p.nrb * (p.keyed * (tiles_of(n, true) + A::kItem) + (p.Hkv - p.keyed) * (tiles_of(n, false) + A::kItem));
+    __device__ __forceinline__ static int item_units(int tiles, bool keyed) {
+        return tiles * (keyed ? A::kUnit : A::kUnitKeyless) + A::kItem;
+    }
+    __device__ __forceinline__ int blocks_of(int rows) const { return p.by_block.div(p.hp * rows + p.block_rows - 1); }
+    __device__ __forceinline__ int seq_units(int n, int rows) const {
+        return blocks_of(rows) * (p.keyed * item_units(tiles_of(n, true), true) +
+                                  (p.entries - p.keyed) * item_units(tiles_of(n, false), false));
     }
     // The item that unit u of a sequence is in; returns its first unit.
-    __device__ __forceinline__ int item_at(int base_u, int n_keys, int unit, Stretch& x) const {
+    __device__ __forceinline__ int item_at(int base_u, int n_keys, int rows, int unit, Stretch& x) const {
+        const int nrb = blocks_of(rows);
         int off = unit - base_u;
         x.n = tiles_of(n_keys, true);
-        const int keyed_units = p.keyed * p.nrb * (x.n + A::kItem);
+        const int keyed_units = p.keyed * nrb * item_units(x.n, true);
         x.keyed = off < keyed_units;
         int first = 0;
         if (!x.keyed) {
@@ -241,19 +257,19 @@ struct AxisWalk {
             off -= keyed_units;
             first = p.keyed;
         }
-        const int block = (int)((unsigned)off / (unsigned)(x.n + A::kItem));
-        x.gi = p.by_nrb.div(block);
-        x.rb = block - x.gi * p.nrb;
-        x.gi += first;
-        return unit - (off - block * (x.n + A::kItem));
+        const int units = item_units(x.n, x.keyed), block = (int)((unsigned)off / (unsigned)units);
+        x.e = nrb == 1 ? block : (int)((unsigned)block / (unsigned)nrb);
+        x.rb = block - x.e * nrb;
+        x.e += first;
+        return unit - (off - block * units);
     }
-    // By a whole warp: lengths are summed a run of sequences per lane.
+    // By a whole warp: units are summed a run of sequences per lane.
     __device__ __forceinline__ AxisWalk(const PagedParams& params, int cta, int grid) : p(params) {
         const int lane = threadIdx.x & 31;
         const int chunk = (p.nseq + 31) >> 5, b_lo = min(lane * chunk, p.nseq), b_hi = min(b_lo + chunk, p.nseq);
         int mine = 0;
 #pragma unroll 4
-        for (int k = b_lo; k < b_hi; ++k) mine += seq_units(key_len<PREFIX>(p, k));
+        for (int k = b_lo; k < b_hi; ++k) mine += seq_units(key_len<PREFIX>(p, k), head_rows<PREFIX>(p, k));
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -272,7 +288,7 @@ struct AxisWalk {
             int at = before, k = b_lo;
             if (lane == src)
                 for (;; ++k) {
-                    const int n = seq_units(key_len<PREFIX>(p, k));
+                    const int n = seq_units(key_len<PREFIX>(p, k), head_rows<PREFIX>(p, k));
                     if (unit < at + n) break;
                     at += n;
                 }
@@ -281,7 +297,8 @@ struct AxisWalk {
         };
         auto snapped = [&](int unit, int seq, int first) {
             Stretch x;
-            const int start = item_at(first, key_len<PREFIX>(p, seq), unit, x), stop = start + A::kItem + x.n;
+            const int start = item_at(first, key_len<PREFIX>(p, seq), head_rows<PREFIX>(p, seq), unit, x);
+            const int stop = start + item_units(x.n, x.keyed);
             return unit - start <= A::kItem + A::kSnap ? start : stop - unit <= A::kSnap ? stop : unit;
         };
         b = base = 0;
@@ -296,21 +313,27 @@ struct AxisWalk {
             }
         }
         len = key_len<PREFIX>(p, b);
+        nr = head_rows<PREFIX>(p, b);
     }
     // The next item of the stretch; false: none left.
     __device__ __forceinline__ bool next(Stretch& x) {
         if (u >= end) return false;
-        while (u >= base + seq_units(len)) {
-            base += seq_units(len);
-            len = key_len<PREFIX>(p, ++b);
+        for (int n; u >= base + (n = seq_units(len, nr));) {
+            base += n;
+            ++b;
+            len = key_len<PREFIX>(p, b);
+            nr = head_rows<PREFIX>(p, b);
         }
-        const int start = item_at(base, len, u, x);
+        const int start = item_at(base, len, nr, u, x), w = x.keyed ? A::kUnit : A::kUnitKeyless;
         x.b = b;
         x.len = len;
-        x.t0 = max(0, u - start - A::kItem);
-        x.t1 = min(x.n, end - start - A::kItem);
-        x.pieces = pieces_of(per, more, A::kItem, A::kSnap, start, x.n, x.c_first);
-        u = start + A::kItem + x.t1;
+        x.n_rows = nr;
+        // a tile belongs to the stretch that holds its first unit
+        x.t0 = max(0, (u - start - A::kItem + w - 1) / w);
+        x.t1 = min(x.n, (end - start - A::kItem + w - 1) / w);
+        x.pieces = pieces_of(per, more, A::kItem, A::kSnap, start, x.n * w, x.c_first);
+        u = start + A::kItem + x.n * w;  // (or past the stretch)
+        if (u > end) u = end;
         return true;
     }
 };
@@ -347,11 +370,31 @@ inline bool make_tmap_pages(const saf_paged_kv& kv, bool keys, int max_rows, CUt
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Units of the longest possible axis must fit 31 bits.
+// Blocks and units of the longest possible axis must fit 31 bits.
 template <class A>
-bool axis_fits(const PagedParams& p) {
-    const double most = A::kItem + std::max(1, (std::max(p.max_len, p.prefix_len) + A::kTile - 1) / A::kTile);
-    return most * p.nrb * p.Hkv * p.nseq < 2147483648.0;
+bool axis_fits(const PagedParams& p, bool prefix) {
+    const double rows = p.hp * (prefix ? (double)p.B * p.T : (double)p.T), blocks = rows / p.block_rows + 1;
+    const double most = A::kItem + A::kUnitKeyless * std::max(1.0, (double)(prefix ? p.prefix_len : p.max_len) / A::kTile + 1);
+    return rows < 2147483648.0 - 256 && most * blocks * p.entries * p.nseq < 2147483648.0;
+}
+// Entries of up to hp heads of one K/V head each; apart: of one kind each.
+inline void make_entries(PagedParams& p, int hp, bool apart) {
+    p.hp = hp;
+    p.entries = 0;
+    for (int want = 0; want < 2; ++want) {  // those that need keys, then those of replaced heads alone
+        for (int g = 0; g < p.Hkv; ++g) {
+            int ordinary = 0;
+            while (ordinary < p.G && !p.replaced.get(p.heads[g * p.G + ordinary])) ++ordinary;
+            const int split = apart || ordinary == 0 ? ordinary : p.G;  // heads of the keyed entries
+            const int from = want ? split : 0, to = want ? p.G : split;
+            for (int u = from; u < to; u += hp, ++p.entries) {
+                p.e_g[p.entries] = (uint8_t)g;
+                p.e_first[p.entries] = (uint8_t)u;
+                p.e_heads[p.entries] = (uint16_t)std::min(hp, to - u);
+            }
+        }
+        if (want == 0) p.keyed = p.entries;
+    }
 }
 // CTAs of either kernel, two per SM; bounds the workspace (pieces: two per CTA).
 constexpr int kMaxGrid = 320;

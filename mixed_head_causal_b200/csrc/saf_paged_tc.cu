@@ -65,12 +65,13 @@ constexpr uint32_t SM_MISC = SM_WARP + 4 * 80;      // TMEM address, last flag, 
 constexpr uint32_t SM_TOTAL = SM_MISC + 40;
 
 struct TcAxis {
-    static constexpr int kTile = BN, kTileKeyless = BN, kItem = 2, kSnap = 2, kMinUnits = 8;
+    // (a block of replaced rows takes about half as long again as one of ordinary rows)
+    static constexpr int kTile = BN, kTileKeyless = BN, kUnit = 2, kUnitKeyless = 3, kItem = 4, kSnap = 4, kMinUnits = 16;
 };
 // An item's stretch as the other warps need it: nt blocks from t0 (those that some
 // row sees; nt < 0: no more items), keyed: some row is ordinary.
 struct TcPiece {
-    int b, gi, rb, len, t0, nt, keyed, pieces, c_first, lb;  // lb: log2 of the rows of a box
+    int b, e, rb, len, n_rows, t0, nt, keyed, pieces, c_first, lb;  // lb: log2 of the rows of a box
 };
 static_assert(sizeof(TcPiece) <= 48, "item slot");
 // What the rows of a warp have in common.  It and the item stay in shared memory
@@ -560,18 +561,18 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             x.nt = -1;
             if (walk.next(w)) {
                 x.b = w.b;
-                x.gi = w.gi;
+                x.e = w.e;
+                x.n_rows = w.n_rows;
                 x.rb = w.rb;
                 x.len = w.len;
                 x.t0 = w.t0;
                 x.pieces = w.pieces;
                 x.c_first = w.c_first;
                 x.lb = lb;
-                const int n = PREFIX ? 0 : new_tokens(p, w.b);
                 int most = 0, ordinary = 0;
 #pragma unroll 1
                 for (int r = lane; r < BM; r += 32) {
-                    const RowInfo row = row_info<PREFIX>(p, w.b, w.gi, w.len, n, p.prefix_len + w.len - n, w.rb * BM + r);
+                    const RowInfo row = row_info<PREFIX>(p, w.b, w.e, w.len, w.n_rows, w.rb * BM + r);
                     most = max(most, row.vis);
                     ordinary |= row.out >= 0 && !row.replaced;
                 }
@@ -588,7 +589,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             if (x.nt < 0) break;
             const int32_t* table = p.table + (size_t)x.b * p.table_stride;
-            const int g = p.order[w.gi];
+            const int g = p.e_g[w.e];
             // pages of this lane's boxes of the last two blocks looked up (block i in entry i & 1)
             int pages[2] = {-1, -1}, looked = 0;
             auto load = [&](int i, bool keys) {
@@ -705,8 +706,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (!ok) break;
             const TcPiece x = items[ni & 1];
             if (x.nt < 0) break;
-            const int n_new = PREFIX ? 0 : new_tokens(p, x.b);
-            const RowInfo info = row_info<PREFIX>(p, x.b, x.gi, x.len, n_new, p.prefix_len + x.len - n_new, x.rb * BM + row);
+            const RowInfo info = row_info<PREFIX>(p, x.b, x.e, x.len, x.n_rows, x.rb * BM + row);
             const bool keyed = x.keyed && x.nt > 0;
             if (keyed) {  // the row's queries (zeros where there are none) in the 128-byte swizzle
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(info.out, 0) * kHeadDim);
@@ -807,7 +807,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     const int c = (row & 3) * 16;  // four threads to a row
 #pragma unroll 1
                     for (int rr = row >> 2; rr < BM; rr += 32) {
-                        const RowInfo y = row_info<PREFIX>(p, x.b, x.gi, x.len, n_new, p.prefix_len + x.len - n_new, x.rb * BM + rr);
+                        const RowInfo y = row_info<PREFIX>(p, x.b, x.e, x.len, x.n_rows, x.rb * BM + rr);
                         float mm = kNegInf;
                         for (int k = 0; k < x.pieces; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + BM * kHeadDim + rr));
                         float4 o[4] = {};
@@ -846,22 +846,26 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 // Joins the pieces of a prefix's items that several CTAs shared: sixteen threads per
 // row.  There is one sequence, of known length, so that the axis is the host's too.
 struct JoinParams {
-    const float* slots;
-    float* part;
-    int rows, part_rows, nrb, tiles, per, more;  // rows of a K/V head
-    Divisor by_rows;
+    PagedParams p;
+    int blocks, tiles, per, more;  // row blocks of an entry
+    Divisor by_blocks;
 };
-__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinParams p) {
+__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinParams j) {
     griddep_launch_dependents();  // (what comes after reads nothing of this call's before it waits in turn)
     griddep_wait();
+    const PagedParams& p = j.p;
     constexpr int SLOT = BM * (kHeadDim + 2);
-    const int row = blockIdx.x * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
-    if (row >= p.part_rows) return;
-    const int gi = p.by_rows.div(row), rr = row - gi * p.rows, in_block = rr & (BM - 1);
+    const int item = blockIdx.x >> 3, in_block = (blockIdx.x & 7) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    const int e = j.by_blocks.div(item), rb = item - e * j.blocks;
+    const int units_o = j.tiles * TcAxis::kUnit + TcAxis::kItem, units_r = j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem;
+    const int before = p.keyed * j.blocks;  // items of keyed entries
+    const int start = item < before ? item * units_o : before * units_o + (item - before) * units_r;
     int first;
-    const int pieces = pieces_of(p.per, p.more, TcAxis::kItem, TcAxis::kSnap,
-                                 (gi * p.nrb + rr / BM) * (p.tiles + TcAxis::kItem), p.tiles, first);
+    const int pieces = pieces_of(j.per, j.more, TcAxis::kItem, TcAxis::kSnap, start,
+                                 j.tiles * (item < before ? TcAxis::kUnit : TcAxis::kUnitKeyless), first);
     if (pieces == 1) return;
+    const RowInfo x = row_info<true>(p, 0, e, p.prefix_len, p.B * p.T, rb * BM + in_block);
+    if (x.out < 0) return;
     auto slot_of = [&](int k) { return p.slots + ((size_t)(first + k) * 2 + (k == 0)) * SLOT; };
     float mm = kNegInf;
 #pragma unroll 8
@@ -876,22 +880,18 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
         o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
         l += f * sl[BM * (kHeadDim + 1) + in_block];
     }
-    *reinterpret_cast<float4*>(p.part + (size_t)row * kHeadDim + c) = o;
-    if (c == 0) {
-        p.part[(size_t)p.part_rows * kHeadDim + row] = mm;
-        p.part[(size_t)p.part_rows * (kHeadDim + 1) + row] = l;
-    }
+    finish_row<true>(p, x, c, o, mm, l);
 }
 
 template <bool PREFIX>
 cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) {
     CUtensorMap mk, mv;
     if (!make_tmap_pages(kv, true, BN, &mk) || !make_tmap_pages(kv, false, BN, &mv)) return cudaErrorNotSupported;
-    p.nrb = (p.rows + BM - 1) / BM;
-    p.by_T = divisor(p.T);
-    p.by_BT = divisor(p.B * p.T);
-    p.by_nrb = divisor(p.nrb);
-    if (!axis_fits<TcAxis>(p)) return cudaErrorNotSupported;
+    // as many heads to an entry as a block has room for
+    make_entries(p, std::max(1, std::min(p.G, BM / (PREFIX ? p.B * p.T : p.T))), true);
+    p.block_rows = BM;
+    p.by_block = divisor(BM);
+    if (!axis_fits<TcAxis>(p, PREFIX)) return cudaErrorNotSupported;
     const int smem = SM_TOTAL;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -911,18 +911,16 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) 
     launch_end(kid, stream);
     if (e != cudaSuccess || !PREFIX) return e != cudaSuccess ? e : cudaGetLastError();
     JoinParams j;  // AxisWalk's own figures
-    j.slots = p.slots;
-    j.part = p.part;
-    j.rows = p.rows;
-    j.part_rows = p.part_rows;
-    j.nrb = p.nrb;
+    j.p = p;
+    j.blocks = (p.hp * p.B * p.T + BM - 1) / BM;
+    j.by_blocks = divisor(j.blocks);
     j.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
-    j.by_rows = divisor(p.rows);
-    const int total = p.Hkv * p.nrb * (j.tiles + TcAxis::kItem);
+    const int total = j.blocks * (p.keyed * (j.tiles * TcAxis::kUnit + TcAxis::kItem) +
+                                  (p.entries - p.keyed) * (j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem));
     const int ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
     j.per = total / ctas;
     j.more = total - j.per * ctas;
-    cfg.gridDim = dim3((unsigned)((p.part_rows + 15) / 16));
+    cfg.gridDim = dim3((unsigned)(p.entries * j.blocks * 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     launch_begin(KID_PAGED_JOIN, stream);
