@@ -332,8 +332,9 @@ SAF_API saf_status saf_rope_table(float *table, int max_pos, int rot_dim, double
  *            pos_offset + position; y0 = x0 cos - x1 sin, y1 = x1 cos + x0 sin in
  *            fp32, rounded once.  rope_len >= pos_offset + max_len.
  *   replaced_mask  host [H], or NULL: every head ordinary.
- * Tokens whose position is outside [0, max_len) are skipped.  Two tokens with
- * the same page and slot: one of the two is kept.  One launch.
+ * Tokens whose position is outside [0, max_len) are skipped.  Two tokens of a
+ * call with the same page and slot: the slot ends as a mixture of the two.
+ * q_out may be q itself where that is contiguous, and k_out k.  One launch.
  */
 SAF_API saf_status saf_kv_append(const saf_paged_kv *kv,
                                  const void *q, const int64_t *q_strides,

@@ -165,6 +165,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     reinterpret_cast<Piece*>(smem + L::ITEM + 48 * slot)->t1 = -1;
                     mbar_arrive(bar_item + 8 * slot);
                 }
+                // A grid in which none has waited may end before the one ahead of it, and the next would start too soon.
+                if (!PREFIX && p.part) griddep_wait();
                 return;
             }
             const int g = p.e_g[w.e], row0 = w.rb * ROWS;

@@ -148,8 +148,9 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
 
 // Scores of 32 keys, chunk c of a block (which goes from 3 to 0), of a row each:
 // the maximum moves if it must (then what the block has written of P so far is
-// scaled along with O and l), P goes to TMEM and its sum to l.  first: O holds
-// nothing yet.
+// scaled along with O and l, and rounded to bf16 once more: another half step of 2^-8
+// on weights that are at most as large as the new maximum's), P goes to TMEM and
+// its sum to l.  first: O holds nothing yet.
 __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool first, float unit, float& m, float& l,
                                           uint32_t tO, uint32_t tP) {
     float mx2[2] = {kNegInf, kNegInf};
@@ -634,6 +635,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
             for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
         }
+        // A grid in which none has waited may end before the one ahead of it, and the next would start too soon.
+        if (!PREFIX && p.part) griddep_wait();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (one elected lane, as in the layer's kernels)
         const uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q (K-major) x K (K-major)
