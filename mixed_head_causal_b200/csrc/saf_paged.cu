@@ -632,7 +632,8 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
 
 template <bool PREFIX>
 cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, cudaStream_t stream) {
-    make_entries(p, p.G, false);
+    p.pad = 1;
+    make_entries(p, p.G, p.G, false);
     p.block_rows = block_rows(PREFIX ? p.B * p.R : p.R);
     p.by_block = divisor(p.block_rows);
     if (!axis_fits<SplitAxis>(p, PREFIX)) return cudaErrorNotSupported;
@@ -679,7 +680,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
             for (int h = g * p.G; h < (g + 1) * p.G; ++h)
                 if (c.replaced.get(h) == (want == 1)) p.heads[at++] = (uint8_t)h;
     p.by_T = divisor(p.T);
-    p.by_BT = divisor(p.B * p.T);
+    p.by_BT = p.by_BT_pad = divisor(p.B * p.T);
     p.err = reinterpret_cast<unsigned int*>(c.ws);
     if (c.prefix_len > 0) {
         p.part = reinterpret_cast<float*>(c.ws + w.part);

@@ -90,12 +90,13 @@ struct PagedParams {
     int B, H, T, G, R, max_len;  // R = G T rows of one (b, g)
     int nseq;                    // key sequences (1 for the prefix)
     // The rows that share keys and an item list: entry e holds e_heads[e] of K/V head e_g[e]'s query heads, from
-    // heads[e_g[e] * G + e_first[e]] on, hp at most.  The keyed ones come first; the others' rows are all replaced.
-    int entries, keyed, hp, block_rows;
+    // heads[e_g[e] * G + e_first[e]] on, hp[0] at most.  The keyed ones come first; the others' rows are all replaced:
+    // hp[1] heads at most, each of a multiple of `pad` rows (those behind its tokens hold nothing).
+    int entries, keyed, hp[2], pad, block_rows;
     uint8_t e_g[kMaxHeads], e_first[kMaxHeads];
     uint16_t e_heads[kMaxHeads];
     uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
-    Divisor by_T, by_BT, by_block;
+    Divisor by_T, by_BT, by_BT_pad, by_block;
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
     // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order K/V
@@ -133,6 +134,8 @@ template <bool PREFIX>
 __device__ __forceinline__ int head_rows(const PagedParams& p, int b) {
     return PREFIX ? p.B * p.T : new_tokens(p, b);
 }
+// n rows of a head with those that fill them up.
+__host__ __device__ __forceinline__ int padded(int n, int pad) { return (n + pad - 1) & -pad; }
 // Row rr of entry e of sequence b, head by head: with PREFIX (head, sequence,
 // token), else (head, token).  len: keys; n: head_rows.
 template <bool PREFIX>
@@ -142,8 +145,12 @@ __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int e, 
     x.vis = x.part = 0;
     x.out = -1;
     x.replaced = 0;
-    if (rr >= p.e_heads[e] * n) return x;
-    const int u = PREFIX ? p.by_BT.div(rr) : n == 1 ? rr : (int)((unsigned)rr / (unsigned)n), rem = rr - u * n;
+    const bool keyed = e < p.keyed;
+    const int np = keyed ? n : padded(n, p.pad);
+    if (rr >= p.e_heads[e] * np) return x;
+    const int u = PREFIX ? (keyed ? p.by_BT : p.by_BT_pad).div(rr) : np == 1 ? rr : (int)((unsigned)rr / (unsigned)np);
+    const int rem = rr - u * np;
+    if (rem >= n) return x;
     const int rb = PREFIX ? p.by_T.div(rem) : b, t = PREFIX ? rem - rb * p.T : rem;
     const int hs = p.e_g[e] * p.G + p.e_first[e] + u, h = p.heads[hs];
     int pos = p.prefix_len + len - n + t;
@@ -239,21 +246,23 @@ struct AxisWalk {
     __device__ __forceinline__ static int item_units(int tiles, bool keyed) {
         return tiles * (keyed ? A::kUnit : A::kUnitKeyless) + A::kItem;
     }
-    __device__ __forceinline__ int blocks_of(int rows) const { return p.by_block.div(p.hp * rows + p.block_rows - 1); }
+    __device__ __forceinline__ int blocks_of(int rows, bool keyed) const {
+        return p.by_block.div((keyed ? p.hp[0] * rows : p.hp[1] * padded(rows, p.pad)) + p.block_rows - 1);
+    }
     __device__ __forceinline__ int seq_units(int n, int rows) const {
-        return blocks_of(rows) * (p.keyed * item_units(tiles_of(n, true), true) +
-                                  (p.entries - p.keyed) * item_units(tiles_of(n, false), false));
+        return p.keyed * blocks_of(rows, true) * item_units(tiles_of(n, true), true) +
+               (p.entries - p.keyed) * blocks_of(rows, false) * item_units(tiles_of(n, false), false);
     }
     // The item that unit u of a sequence is in; returns its first unit.
     __device__ __forceinline__ int item_at(int base_u, int n_keys, int rows, int unit, Stretch& x) const {
-        const int nrb = blocks_of(rows);
-        int off = unit - base_u;
+        int nrb = blocks_of(rows, true), off = unit - base_u;
         x.n = tiles_of(n_keys, true);
         const int keyed_units = p.keyed * nrb * item_units(x.n, true);
         x.keyed = off < keyed_units;
         int first = 0;
         if (!x.keyed) {
             x.n = tiles_of(n_keys, false);
+            nrb = blocks_of(rows, false);
             off -= keyed_units;
             first = p.keyed;
         }
@@ -373,13 +382,15 @@ inline bool make_tmap_pages(const saf_paged_kv& kv, bool keys, int max_rows, CUt
 // Blocks and units of the longest possible axis must fit 31 bits.
 template <class A>
 bool axis_fits(const PagedParams& p, bool prefix) {
-    const double rows = p.hp * (prefix ? (double)p.B * p.T : (double)p.T), blocks = rows / p.block_rows + 1;
+    const double rows = (double)std::max(p.hp[0], p.hp[1]) * ((prefix ? (double)p.B * p.T : (double)p.T) + p.pad - 1);
+    const double blocks = rows / p.block_rows + 1;
     const double most = A::kItem + A::kUnitKeyless * std::max(1.0, (double)(prefix ? p.prefix_len : p.max_len) / A::kTile + 1);
     return rows < 2147483648.0 - 256 && most * blocks * p.entries * p.nseq < 2147483648.0;
 }
-// Entries of up to hp heads of one K/V head each; apart: of one kind each.
-inline void make_entries(PagedParams& p, int hp, bool apart) {
-    p.hp = hp;
+// Entries of up to hp heads of one K/V head each, hp_replaced where none of them is ordinary; apart: of one kind each.
+inline void make_entries(PagedParams& p, int hp, int hp_replaced, bool apart) {
+    p.hp[0] = hp;
+    p.hp[1] = hp_replaced;
     p.entries = 0;
     for (int want = 0; want < 2; ++want) {  // those that need keys, then those of replaced heads alone
         for (int g = 0; g < p.Hkv; ++g) {
@@ -387,10 +398,11 @@ inline void make_entries(PagedParams& p, int hp, bool apart) {
             while (ordinary < p.G && !p.replaced.get(p.heads[g * p.G + ordinary])) ++ordinary;
             const int split = apart || ordinary == 0 ? ordinary : p.G;  // heads of the keyed entries
             const int from = want ? split : 0, to = want ? p.G : split;
-            for (int u = from; u < to; u += hp, ++p.entries) {
+            const int most = p.hp[want];
+            for (int u = from; u < to; u += most, ++p.entries) {
                 p.e_g[p.entries] = (uint8_t)g;
                 p.e_first[p.entries] = (uint8_t)u;
-                p.e_heads[p.entries] = (uint16_t)std::min(hp, to - u);
+                p.e_heads[p.entries] = (uint16_t)std::min(most, to - u);
             }
         }
         if (want == 0) p.keyed = p.entries;

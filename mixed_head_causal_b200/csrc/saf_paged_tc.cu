@@ -88,7 +88,8 @@ struct WarpRows {
     int pure;              // all rows with a token look up, by one head's vectors
     int low, span;         // from r on: the lowest of their stretches, and from there to the highest
     int low_edge;          // the 16-byte boundary at or before the lowest's entry of local key 127
-    int room;              // floats of the array past r
+    int room, before;      // floats of the array from r on, and before it (2^30 at most)
+    int last;              // the last key
     int vmin;              // keys that every row sees
 };
 static_assert(sizeof(WarpRows) <= 80, "warp slot");
@@ -210,27 +211,32 @@ __device__ __forceinline__ void add_a(float* v, const float* a) {
     }
 }
 
-// A block of a warp whose rows are all replaced, of one head, and see every key of
-// it, their stretches of r at most NEAR_SPAN apart (a chunk's tokens, sequences of
-// like lengths): one stretch serves them all, copied a block ahead.  off: this
-// row's against the lowest.  primed: the block's copies are under way; next: the
-// block after it is of this kind, and its copies are started.  Returns (m, l).
+// A block of a warp whose rows are all replaced and of one head, their stretches of
+// r at most NEAR_SPAN apart (a chunk's tokens, sequences of like lengths): one
+// stretch serves them all, copied a block ahead.  off: this row's against the
+// first's.  primed: the block's copies are under way; next: there is a block after
+// it, and its copies are started.  masked: not every row sees every key (vis, and
+// boxes without a page in `bad`); what lies before the array or past the last key is
+// then not copied.  Returns (m, l).
 __device__ __forceinline__ void near_copy(int k0) {
     const WarpRows& w = warp_rows();
     const int lane = threadIdx.x & 31;
     const uint32_t buf = smem_addr(staging()) + (uint32_t)((k0 / BN) & 1) * NEAR_BUF * 4;
-    const float *a = w.a + k0 + lane, *r = w.r - k0;
+    const float* r = w.r - k0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, a + 32 * i);
+    for (int i = 0; i < 4; ++i) copy4(buf + (32 * i + lane) * 4, w.a + min(k0 + 32 * i + lane, w.last));
     // from the boundary at or before the lowest row's last key to the highest row's first key
     const int edge = w.low_edge, stop = w.low + w.span + 1;
     for (int at = edge + 4 * lane; at < stop; at += 128) {
-        const int bytes = min(4, w.room + k0 - at) * 4;  // (the last may reach past the array)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(buf + (128 + at - edge) * 4), "l"(r + at), "r"(bytes));
+        const bool in = at - k0 + w.before >= 0;
+        const int bytes = in ? min(4, w.room + k0 - at) * 4 : 0;  // (the last may reach past the array)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(buf + (128 + at - edge) * 4),
+                     "l"(in ? r + at : w.r0), "r"(bytes));
     }
     copies_commit();
 }
-__device__ __noinline__ float2 near_block(float m, float l, bool primed, bool next, bool first, int off, uint32_t tmem, int k0) {
+__device__ __noinline__ float2 near_block(float m, float l, bool primed, bool next, bool first, int off, uint32_t tmem, int k0,
+                                          bool masked, int vis, uint32_t bad, int lb) {
     if (!primed) near_copy(k0);
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncwarp();
@@ -242,6 +248,12 @@ __device__ __noinline__ float2 near_block(float m, float l, bool primed, bool ne
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = r[-32 * c - e];
         add_a<32>(v, a + 32 * c);
+        if (masked) {
+            const int left = vis - k0 - 32 * c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = kNegInf;
+        }
         chunk_out(v, c, first, kLog2e, m, l, tmem + TO_COL, tmem + TP_COL);
     }
     __syncwarp();  // the buffer has been read
@@ -296,8 +308,8 @@ __device__ __noinline__ float2 far_block(float m, float l, bool primed, bool nex
     return make_float2(m, l);
 }
 
-// A block of a warp that is neither that nor plain: it holds both kinds, or there are
-// keys that a row does not see.  32 keys at a time, in a loop (a cold unrolled
+// A block of a warp that is none of these: several heads' rows, both kinds, or keys
+// that a row does not see.  32 keys at a time, in a loop (a cold unrolled
 // copy would cost more to fetch than to run).  Returns (m, l).
 __device__ __noinline__ float2 mixed_block(float m, float l, float unit, int vis, bool first, uint32_t tmem, int ni, int k0,
                                            uint32_t bad) {
@@ -472,10 +484,12 @@ __device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tme
         if (!ok) break;
         const WarpRows& w = warp_rows();
         float2 ml;
-        if (w.pure && k0 + BN <= w.vmin && !bad) {
-            const bool next = i + 1 < nt;
-            ml = w.span <= NEAR_SPAN ? near_block(m, l, primed, next, i == 0, off, tmem, k0)
-                                     : far_block(m, l, primed, next, i == 0, off, edge, tmem, k0);
+        const bool next = i + 1 < nt, masked = k0 + BN > w.vmin || bad;
+        if (w.pure && w.span <= NEAR_SPAN) {
+            ml = near_block(m, l, primed, next, i == 0, off, tmem, k0, masked, vis, bad, item_of(ni).lb);
+            primed = next;
+        } else if (w.pure && !masked) {
+            ml = far_block(m, l, primed, next, i == 0, off, edge, tmem, k0);
             primed = next;
         } else {
             if (primed) {  // copies begun for this block: its staging area is wanted
@@ -752,6 +766,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 w.low_edge = (int)(((r_first + low - 127) & ~3ll) - r_first);
                 w.span = span;
                 w.room = (int)min((long long)p.H * p.pattern_len - r_first, 1ll << 30);
+                w.before = (int)min(r_first, 1ll << 30);
+                w.last = max(x.len, 1) - 1;
                 w.vmin = vmin;
             }
             __syncwarp();
@@ -850,8 +866,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 // row.  There is one sequence, of known length, so that the axis is the host's too.
 struct JoinParams {
     PagedParams p;
-    int blocks, tiles, per, more;  // row blocks of an entry
-    Divisor by_blocks;
+    int blocks[2], tiles, per, more;  // row blocks of a keyed entry and of the others
+    Divisor by_blocks[2];
 };
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinParams j) {
     griddep_launch_dependents();  // (what comes after reads nothing of this call's before it waits in turn)
@@ -859,13 +875,14 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     const PagedParams& p = j.p;
     constexpr int SLOT = BM * (kHeadDim + 2);
     const int item = blockIdx.x >> 3, in_block = (blockIdx.x & 7) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
-    const int e = j.by_blocks.div(item), rb = item - e * j.blocks;
     const int units_o = j.tiles * TcAxis::kUnit + TcAxis::kItem, units_r = j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem;
-    const int before = p.keyed * j.blocks;  // items of keyed entries
-    const int start = item < before ? item * units_o : before * units_o + (item - before) * units_r;
+    const int before = p.keyed * j.blocks[0];  // items of keyed entries
+    const int kind = item >= before, nth = kind ? item - before : item;  // (among the items of its kind)
+    const int e_nth = j.by_blocks[kind].div(nth), rb = nth - e_nth * j.blocks[kind], e = kind ? p.keyed + e_nth : e_nth;
+    const int start = kind ? before * units_o + nth * units_r : nth * units_o;
     int first;
     const int pieces = pieces_of(j.per, j.more, TcAxis::kItem, TcAxis::kSnap, start,
-                                 j.tiles * (item < before ? TcAxis::kUnit : TcAxis::kUnitKeyless), first);
+                                 j.tiles * (kind ? TcAxis::kUnitKeyless : TcAxis::kUnit), first);
     if (pieces == 1) return;
     const RowInfo x = row_info<true>(p, 0, e, p.prefix_len, p.B * p.T, rb * BM + in_block);
     if (x.out < 0) return;
@@ -890,8 +907,12 @@ template <bool PREFIX>
 cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) {
     CUtensorMap mk, mv;
     if (!make_tmap_pages(kv, true, BN, &mk) || !make_tmap_pages(kv, false, BN, &mv)) return cudaErrorNotSupported;
-    // as many heads to an entry as a block has room for
-    make_entries(p, std::max(1, std::min(p.G, BM / (PREFIX ? p.B * p.T : p.T))), true);
+    // as many heads to an entry as a block has room for; replaced heads begin with a warp (see near_block)
+    const int rows = PREFIX ? p.B * p.T : p.T;
+    p.pad = 32;
+    auto heads = [&](int n) { return std::max(1, std::min(p.G, BM / n)); };
+    make_entries(p, heads(rows), heads(padded(rows, p.pad)), true);
+    p.by_BT_pad = divisor(padded(p.B * p.T, p.pad));
     p.block_rows = BM;
     p.by_block = divisor(BM);
     if (!axis_fits<TcAxis>(p, PREFIX)) return cudaErrorNotSupported;
@@ -915,15 +936,16 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) 
     if (e != cudaSuccess || !PREFIX) return e != cudaSuccess ? e : cudaGetLastError();
     JoinParams j;  // AxisWalk's own figures
     j.p = p;
-    j.blocks = (p.hp * p.B * p.T + BM - 1) / BM;
-    j.by_blocks = divisor(j.blocks);
+    j.blocks[0] = (p.hp[0] * rows + BM - 1) / BM;
+    j.blocks[1] = (p.hp[1] * padded(rows, p.pad) + BM - 1) / BM;
+    for (int k = 0; k < 2; ++k) j.by_blocks[k] = divisor(j.blocks[k]);
+    const int items[2] = {p.keyed * j.blocks[0], (p.entries - p.keyed) * j.blocks[1]};
     j.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
-    const int total = j.blocks * (p.keyed * (j.tiles * TcAxis::kUnit + TcAxis::kItem) +
-                                  (p.entries - p.keyed) * (j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem));
+    const int total = items[0] * (j.tiles * TcAxis::kUnit + TcAxis::kItem) + items[1] * (j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem);
     const int ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
     j.per = total / ctas;
     j.more = total - j.per * ctas;
-    cfg.gridDim = dim3((unsigned)(p.entries * j.blocks * 8));
+    cfg.gridDim = dim3((unsigned)((items[0] + items[1]) * 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     launch_begin(KID_PAGED_JOIN, stream);
