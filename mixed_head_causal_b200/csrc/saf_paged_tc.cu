@@ -109,24 +109,29 @@ __device__ __forceinline__ const volatile TcPiece& item_of(int ni) {
 __device__ __forceinline__ const WarpRows& warp_rows() { return reinterpret_cast<WarpRows*>(smem_base() + SM_WARP)[quarter_of()]; }
 __device__ __forceinline__ float* staging() { return reinterpret_cast<float*>(smem_base() + SM_PAT + quarter_of() * PAT_BYTES); }
 
-// Row max of 128 raw scores: three-input max, four independent chains.
-__device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
-    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+// The values of a TMEM load pass through here once the load has been waited for, so
+// that nothing made of them moves ahead of the wait.
+__device__ __forceinline__ void loaded(uint32_t (&v)[32]) {
+    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+    asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
+}
+// Maxima of 32 raw scores into two independent chains of three-input max.
+__device__ __forceinline__ void quarter_max(const uint32_t (&v)[32], float (&mx)[2]) {
 #pragma unroll
-    for (int e = 0; e < 128; e += 2)
-        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
 }
 
 // P = exp2(s * unit - m * unit) of keys [32 Q, 32 Q + 32) as 16 bf16 pairs, their sum added to l2.
 template <int Q>
-__device__ __forceinline__ void exp_quarter(const uint32_t (&v)[128], uint64_t unit2, uint64_t nm2, uint64_t (&l2)[4],
+__device__ __forceinline__ void exp_quarter(const uint32_t (&v)[32], uint64_t unit2, uint64_t nm2, uint64_t (&l2)[4],
                                             uint32_t tP) {
     uint32_t pw[16];
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
         const float2 x =
-            split_f32x2(fma_f32x2(f32x2(__uint_as_float(v[32 * Q + e]), __uint_as_float(v[32 * Q + e + 1])), unit2, nm2));
+            split_f32x2(fma_f32x2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), unit2, nm2));
         const float p0 = ex2(x.x), p1 = ex2(x.y);
         l2[(e >> 1) & 3] = add_f32x2(l2[(e >> 1) & 3], f32x2(p0, p1));
         pw[e >> 1] = pack_bf16x2(p0, p1);
@@ -380,10 +385,10 @@ constexpr uint32_t SM_KMETA = SM_MISC + 8, SM_VMETA = SM_MISC + 24;
 
 // Block i of item ni has landed, with its scores where it has some; boxes without a
 // page in `bad`.  nk, nv: S and P V products before it.
-__device__ __forceinline__ bool block_arrived(int ni, int nk, int nv, uint32_t& bad) {
+__device__ __forceinline__ bool block_arrived(bool keyed, int nk, int nv, uint32_t& bad) {
     const uint32_t sbase = smem_addr(smem_base());
     bool ok;
-    if (item_of(ni).keyed) {
+    if (keyed) {
         // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load was
         // seen by the MMA warp before it issued S)
         ok = mbar_wait_warp(sbase + BAR_S, nk & 1, kWaitLimit);
@@ -402,9 +407,9 @@ __device__ __forceinline__ bool p_free(bool first, int nv) {
     tc_fence_after();
     return ok;
 }
-__device__ __forceinline__ void s_copied(int ni) {  // the MMA warp may now overwrite S
+__device__ __forceinline__ void s_copied(bool keyed) {  // the MMA warp may now overwrite S
     tc_fence_before();
-    if (item_of(ni).keyed) mbar_arrive_warp(smem_addr(smem_base()) + BAR_SF);
+    if (keyed) mbar_arrive_warp(smem_addr(smem_base()) + BAR_SF);
 }
 __device__ __forceinline__ void hand_over() {
     tmem_wait_st();
@@ -414,9 +419,10 @@ __device__ __forceinline__ void hand_over() {
 // Slots without a token may hold a NaN, and 0 times that is one: their V rows become
 // zeros before P V reads them.
 __device__ __forceinline__ bool clear_dead(int ni, int nv, int k0, uint32_t bad) {
-    const uint32_t sbase = smem_addr(smem_base());
-    const int len = item_of(ni).len, row = quarter_of() * 32 + (threadIdx.x & 31);
+    const int len = item_of(ni).len;
     if (k0 + BN <= len && !bad) return true;
+    const uint32_t sbase = smem_addr(smem_base());
+    const int row = quarter_of() * 32 + (threadIdx.x & 31);
     const bool ok = mbar_wait_warp(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
     if (k0 + row >= len || ((bad >> (row >> item_of(ni).lb)) & 1u)) {
 #pragma unroll
@@ -429,25 +435,39 @@ __device__ __forceinline__ bool clear_dead(int ni, int nv, int k0, uint32_t bad)
 // The blocks of a warp without rows that look scores up.  tmem: of this warp's lanes.
 __device__ __noinline__ RowResult plain_rows(float unit, int vis, uint32_t tmem, int ni, int nk, int nv) {
     float m = kNegInf, l = 0.f;
-    int k0 = (item_of(ni).t0 + item_of(ni).nt) * BN;
-    for (int i = 0; i < item_of(ni).nt; ++i, ++nk, ++nv) {
+    const int nt = item_of(ni).nt, vmin = warp_rows().vmin;
+    const bool keyed = item_of(ni).keyed;
+    int k0 = (item_of(ni).t0 + nt) * BN;
+    for (int i = 0; i < nt; ++i, ++nk, ++nv) {
         k0 -= BN;
         uint32_t bad;
-        if (!block_arrived(ni, nk, nv, bad)) return {m, l, 0};
-        if (k0 + BN > warp_rows().vmin || bad) {
+        if (!block_arrived(keyed, nk, nv, bad)) return {m, l, 0};
+        if (k0 + BN > vmin || bad) {
             if (!p_free(i == 0, nv)) return {m, l, 0};
             const float2 ml = mixed_block(m, l, unit, vis, i == 0, tmem, ni, k0, bad);
             m = ml.x;
             l = ml.y;
-            s_copied(ni);
+            s_copied(keyed);
             if (!clear_dead(ni, nv, k0, bad)) return {m, l, 0};
         } else {
-            uint32_t v[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+            // The scores of keys 64..127 stay in registers, the others are loaded again for their exponentials: all
+            // 128 with what the exponentials need would not fit 168 registers.
+            uint32_t v[2][32], w[2][32];
+            tmem_ld32(tmem, w[0]);
+            tmem_ld32(tmem + 32, w[1]);
+            tmem_ld32(tmem + 64, v[0]);
+            tmem_ld32(tmem + 96, v[1]);
             tmem_wait_ld();
-            s_copied(ni);
-            const float mx = row_max(v);
+            loaded(w[0]);
+            loaded(w[1]);
+            loaded(v[0]);
+            loaded(v[1]);
+            float ma[2] = {kNegInf, kNegInf}, mb[2] = {kNegInf, kNegInf};
+            quarter_max(w[0], ma);
+            quarter_max(w[1], mb);
+            quarter_max(v[0], ma);
+            quarter_max(v[1], mb);
+            const float mx = fmaxf(fmaxf(ma[0], ma[1]), fmaxf(mb[0], mb[1]));
             float f = 1.f;
             if ((mx - m) * unit > 8.f) {
                 f = ex2((m - mx) * unit);
@@ -458,10 +478,16 @@ __device__ __noinline__ RowResult plain_rows(float unit, int vis, uint32_t tmem,
             const float nm = m == kNegInf ? 0.f : -m * unit;
             const uint64_t unit2 = f32x2(unit, unit), nm2 = f32x2(nm, nm);
             uint64_t l2[4] = {0, 0, 0, 0};
-            exp_quarter<0>(v, unit2, nm2, l2, tmem + TP_COL);
-            exp_quarter<1>(v, unit2, nm2, l2, tmem + TP_COL);
-            exp_quarter<2>(v, unit2, nm2, l2, tmem + TP_COL);
-            exp_quarter<3>(v, unit2, nm2, l2, tmem + TP_COL);
+            tmem_ld32(tmem, w[0]);
+            exp_quarter<2>(v[0], unit2, nm2, l2, tmem + TP_COL);
+            tmem_ld32(tmem + 32, w[1]);
+            exp_quarter<3>(v[1], unit2, nm2, l2, tmem + TP_COL);
+            tmem_wait_ld();
+            loaded(w[0]);
+            loaded(w[1]);
+            s_copied(keyed);
+            exp_quarter<0>(w[0], unit2, nm2, l2, tmem + TP_COL);
+            exp_quarter<1>(w[1], unit2, nm2, l2, tmem + TP_COL);
             const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
             l += s2.x + s2.y;
             if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tmem + TO_COL, f);
@@ -476,11 +502,12 @@ __device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tme
     float m = kNegInf, l = 0.f;
     bool primed = false, ok = true;
     const int nt = item_of(ni).nt;
+    const bool keyed = item_of(ni).keyed;
     int k0 = (item_of(ni).t0 + nt) * BN;
     for (int i = 0; ok && i < nt; ++i, ++nk, ++nv) {
         k0 -= BN;
         uint32_t bad;
-        ok = block_arrived(ni, nk, nv, bad) && p_free(i == 0, nv);
+        ok = block_arrived(keyed, nk, nv, bad) && p_free(i == 0, nv);
         if (!ok) break;
         const WarpRows& w = warp_rows();
         float2 ml;
@@ -501,7 +528,7 @@ __device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tme
         }
         m = ml.x;
         l = ml.y;
-        s_copied(ni);
+        s_copied(keyed);
         ok = clear_dead(ni, nv, k0, bad);
         hand_over();
     }
@@ -823,27 +850,45 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 if (ok && *last_flag) {
                     __threadfence();
                     auto slot_of = [&](int k) { return p.slots + ((size_t)(x.c_first + k) * 2 + (k == 0)) * SLOT; };
-                    const int c = (row & 3) * 16;  // four threads to a row
+                    // the rows' maxima and sums by a thread each, then their columns by four threads to a row; loads of
+                    // four pieces at a time
+                    float2* sums = reinterpret_cast<float2*>(smem + SM_PAT);
+                    float mm = kNegInf, ll = 0.f;
+#pragma unroll 4
+                    for (int k = 0; k < x.pieces; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + BM * kHeadDim + row));
+#pragma unroll 4
+                    for (int k = 0; k < x.pieces; ++k)
+                        ll += weight(__ldcg(slot_of(k) + BM * kHeadDim + row), mm) * __ldcg(slot_of(k) + BM * (kHeadDim + 1) + row);
+                    sums[row] = make_float2(mm, ll);
+                    join_warps();
+                    const int c = (row & 3) * 16;
 #pragma unroll 1
                     for (int rr = row >> 2; rr < BM; rr += 32) {
                         const RowInfo y = row_info<PREFIX>(p, x.b, x.e, x.len, x.n_rows, x.rb * BM + rr);
-                        float mm = kNegInf;
-                        for (int k = 0; k < x.pieces; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + BM * kHeadDim + rr));
+                        const float2 ml = sums[rr];
                         float4 o[4] = {};
-                        float ll = 0.f;
-#pragma unroll 2
-                        for (int k = 0; k < x.pieces; ++k) {
-                            const float* sl = slot_of(k);
-                            const float fk = weight(__ldcg(sl + BM * kHeadDim + rr), mm);
-                            ll += fk * __ldcg(sl + BM * (kHeadDim + 1) + rr);
+                        for (int k = 0; k < x.pieces; k += 4) {
+                            float f[4];
+                            float4 v[4][4];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c + 4 * q));
-                                o[q] = make_float4(o[q].x + fk * v.x, o[q].y + fk * v.y, o[q].z + fk * v.z, o[q].w + fk * v.w);
+                            for (int u = 0; u < 4; ++u) {
+                                const float* sl = slot_of(min(k + u, x.pieces - 1));
+                                f[u] = k + u < x.pieces ? __ldcg(sl + BM * kHeadDim + rr) : kNegInf;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) v[u][q] = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c + 4 * q));
+                            }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                if (k + u >= x.pieces) break;
+                                const float fk = weight(f[u], ml.x);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    o[q] = make_float4(o[q].x + fk * v[u][q].x, o[q].y + fk * v[u][q].y, o[q].z + fk * v[u][q].z,
+                                                       o[q].w + fk * v[u][q].w);
                             }
                         }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) finish_row<PREFIX>(p, y, c + 4 * q, o[q], mm, ll);
+                        for (int q = 0; q < 4; ++q) finish_row<PREFIX>(p, y, c + 4 * q, o[q], ml.x, ml.y);
                     }
                     if (row == 0) atomicExch(p.counters + x.c_first, 0u);
                 }
