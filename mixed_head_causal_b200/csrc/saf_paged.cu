@@ -583,10 +583,10 @@ int block_rows(int rows) { return ((rows + row_blocks(rows) - 1) / row_blocks(ro
 // Items of more rows than this go to the tensor-core kernel.
 constexpr int kTcRows = 32;
 
-// Workspace: header, the two launches' piece counters and pieces, the prefix's
-// parts.  Sizes grow with each argument.
+// Workspace: header, the two launches' piece counters, shared items and pieces,
+// the prefix's parts.  Sizes grow with each argument.
 struct PagedWs {
-    size_t counters[2], slots[2], part, total;
+    size_t counters[2], shared[2], slots[2], part, total;
 };
 PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
     PagedWs w{};
@@ -596,6 +596,11 @@ PagedWs paged_ws(int B, int H, int H_kv, int T, int prefix_len) {
         w.counters[k] = off;
         off += kMaxGrid * sizeof(unsigned int);
     }
+    for (int k = 0; k < 2; ++k) {
+        w.shared[k] = off = align256(off);
+        off += kMaxGrid * sizeof(SharedItem);
+    }
+    off = align256(off);
     for (int k = 0; k < (prefix_len > 0 ? 2 : 1); ++k) {
         const int rows = k ? B * R : R, most = rows > kTcRows ? 128 : (rows + 7) & ~7;
         w.slots[k] = off;
@@ -690,6 +695,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
         p.nseq = 1;
         p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[1]);
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
+        p.shared = reinterpret_cast<SharedItem*>(c.ws + w.shared[1]);
         const cudaError_t e = c.B * p.R > kTcRows ? launch_paged_tc(c.kv, p, true, stream)
                                                : launch_split_rows<true>(mk, mv, p, stream);
         if (e != cudaSuccess) return e;
@@ -699,6 +705,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.nseq = c.B;
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
+    p.shared = reinterpret_cast<SharedItem*>(c.ws + w.shared[0]);
     if (p.R <= kTcRows) return launch_split_rows<false>(mk, mv, p, stream);
     return launch_paged_tc(c.kv, p, false, stream);
 }

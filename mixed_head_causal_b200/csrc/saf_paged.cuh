@@ -77,6 +77,11 @@ struct RowInfo {
     int replaced;   // its head + 1, or 0
 };
 
+// The item of several pieces whose first is this CTA's (pieces = 0: none).
+struct __align__(16) SharedItem {
+    int pieces, b, e, rb, len, n_rows, unused[2];
+};
+
 // What the attention kernels need, by value.
 struct PagedParams {
     const __nv_bfloat16* q;
@@ -99,6 +104,7 @@ struct PagedParams {
     Divisor by_T, by_BT, by_BT_pad, by_block;
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
+    SharedItem* shared;          // per CTA, of the tensor-core kernel
     // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order K/V
     // head (by order[]), head of the group, sequence, token.
     float* part;

@@ -5,11 +5,10 @@
 // with a shared prefix times the sequences), its keys in blocks of 128, last block
 // first (patterns tend to favour near keys: the running maximum then starts near
 // where it ends).  The blocks of all items form one axis, of which every CTA of two
-// per SM takes an equal stretch, as in the kernel for few rows (saf_paged.cu).  An
-// item that several share is joined by the CTA that finishes its last piece, in
-// key order, or with a prefix, whose few items are cut into many pieces, by a
-// launch of its own with a thread per four columns of every row (one CTA took 50 us
-// over 18 pieces of 128 rows).  Six warps:
+// per SM takes an equal stretch, as in the kernel for few rows (saf_paged.cu).  The
+// pieces of an item that several share are joined by a launch of its own, with a
+// thread per four columns of every row: the CTA that finishes an item's last piece
+// took 13 us over 4 pieces of 128 rows, 50 us over 18.  Six warps:
 //   warp 0      producer: walks the stretch, page look-up and TMA loads, a box per
 //               page, two stages each of K and V (no K where all rows are replaced)
 //   warp 1      TMEM owner and MMA issuer (one elected lane):
@@ -61,12 +60,12 @@ constexpr uint32_t SM_ROW = SM_PAT + 4 * PAT_BYTES;  // [128] {head, r at local 
 constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
 constexpr uint32_t SM_ITEM = SM_BAR + 20 * 8;       // [2] TcPiece
 constexpr uint32_t SM_WARP = SM_ITEM + 2 * 48;      // [4] WarpRows
-constexpr uint32_t SM_MISC = SM_WARP + 4 * 80;      // TMEM address, last flag, [4] boxes of a K load without a page, [4] of a V load
+constexpr uint32_t SM_MISC = SM_WARP + 4 * 80;      // TMEM address, [4] boxes of a K load without a page, [4] of a V load
 constexpr uint32_t SM_TOTAL = SM_MISC + 40;
 
 struct TcAxis {
-    // (a block of replaced rows takes about half as long again as one of ordinary rows)
-    static constexpr int kTile = BN, kTileKeyless = BN, kUnit = 2, kUnitKeyless = 3, kItem = 4, kSnap = 4, kMinUnits = 16;
+    // (a block of replaced rows takes about twice as long as one of ordinary rows: 3.6 us against 1.8, two CTAs per SM)
+    static constexpr int kTile = BN, kTileKeyless = BN, kUnit = 2, kUnitKeyless = 4, kItem = 4, kSnap = 4, kMinUnits = 16;
 };
 // An item's stretch as the other warps need it: nt blocks from t0 (those that some
 // row sees; nt < 0: no more items), keyed: some row is ordinary.
@@ -379,8 +378,7 @@ constexpr uint32_t BAR_S = BAR_Q + 8;                               // S ready
 constexpr uint32_t BAR_SF = BAR_S + 8;                              // S copied out by the rows (4 warp arrivals)
 constexpr uint32_t BAR_P = BAR_SF + 8;                              // P written (4 warp arrivals)
 constexpr uint32_t BAR_O = BAR_P + 8;                               // P V done
-constexpr uint32_t BAR_JOIN = BAR_O + 8;                            // row warps together (4 warp arrivals)
-static_assert(BAR_JOIN + 8 <= SM_ITEM, "barrier area");
+static_assert(BAR_O + 8 <= SM_ITEM, "barrier area");
 constexpr uint32_t SM_KMETA = SM_MISC + 8, SM_VMETA = SM_MISC + 24;
 
 // Block i of item ni has landed, with its scores where it has some; boxes without a
@@ -545,18 +543,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const uint32_t sbase = smem_addr(smem);
     const uint32_t bar_kf = sbase + BAR_KF, bar_ke = sbase + BAR_KE, bar_vf = sbase + BAR_VF, bar_ve = sbase + BAR_VE;
     const uint32_t bar_item = sbase + BAR_ITEM, bar_taken = sbase + BAR_TAKEN, bar_q = sbase + BAR_Q, bar_s = sbase + BAR_S;
-    const uint32_t bar_sf = sbase + BAR_SF, bar_p = sbase + BAR_P, bar_o = sbase + BAR_O, bar_join = sbase + BAR_JOIN;
+    const uint32_t bar_sf = sbase + BAR_SF, bar_p = sbase + BAR_P, bar_o = sbase + BAR_O;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SM_MISC);
-    volatile int* last_flag = reinterpret_cast<int*>(smem + SM_MISC + 4);
     volatile uint32_t *kmeta = reinterpret_cast<uint32_t*>(smem + SM_KMETA),
                       *vmeta = reinterpret_cast<uint32_t*>(smem + SM_VMETA);
     TcPiece* items = reinterpret_cast<TcPiece*>(smem + SM_ITEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
     if (sbase & 1023u) {  // the swizzled tiles need what the declaration asks for
-        if (threadIdx.x == 0) report(p.err, 0x504);
+        griddep_wait();
+        if (threadIdx.x == 0) {
+            p.shared[blockIdx.x].pieces = 0;
+            report(p.err, 0x504);
+        }
         return;
     }
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(bar_kf + 8 * s, 1);
@@ -571,7 +572,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         mbar_init(bar_sf, 4);
         mbar_init(bar_p, 4);
         mbar_init(bar_o, 1);
-        mbar_init(bar_join, 4);
         fence_mbar_init();
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -737,14 +737,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // ------------------------------------------------ row threads
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t tmem_rows = tmem + ((uint32_t)(quarter * 32) << 16), tO = tmem_rows + TO_COL;
-        int nk = 0, nv = 0, joins = 0;  // S and P V products, joins of the row warps so far
+        int nk = 0, nv = 0;  // S and P V products so far
         bool ok = true, waited = false;
-        // A barrier of the row warps, bounded like every wait.
-        auto join_warps = [&] {
-            mbar_arrive_warp(bar_join);
-            if (ok) ok = mbar_wait_warp(bar_join, joins & 1, kWaitLimit);
-            ++joins;
-        };
+        if (row == 0) p.shared[blockIdx.x].pieces = 0;  // until there is one
         for (int ni = 0; ok; ++ni) {
             ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
             if (!ok) break;
@@ -842,58 +837,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 __stcg(slot + BM * kHeadDim + row, m);
                 __stcg(slot + BM * (kHeadDim + 1) + row, l);
             }
-            if (!PREFIX && x.pieces > 1) {
-                __threadfence();
-                join_warps();
-                if (row == 0) *last_flag = atomicAdd(p.counters + x.c_first, 1u) == (unsigned)x.pieces - 1;
-                join_warps();
-                if (ok && *last_flag) {
-                    __threadfence();
-                    auto slot_of = [&](int k) { return p.slots + ((size_t)(x.c_first + k) * 2 + (k == 0)) * SLOT; };
-                    // the rows' maxima and sums by a thread each, then their columns by four threads to a row; loads of
-                    // four pieces at a time
-                    float2* sums = reinterpret_cast<float2*>(smem + SM_PAT);
-                    float mm = kNegInf, ll = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < x.pieces; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + BM * kHeadDim + row));
-#pragma unroll 4
-                    for (int k = 0; k < x.pieces; ++k)
-                        ll += weight(__ldcg(slot_of(k) + BM * kHeadDim + row), mm) * __ldcg(slot_of(k) + BM * (kHeadDim + 1) + row);
-                    sums[row] = make_float2(mm, ll);
-                    join_warps();
-                    const int c = (row & 3) * 16;
-#pragma unroll 1
-                    for (int rr = row >> 2; rr < BM; rr += 32) {
-                        const RowInfo y = row_info<PREFIX>(p, x.b, x.e, x.len, x.n_rows, x.rb * BM + rr);
-                        const float2 ml = sums[rr];
-                        float4 o[4] = {};
-                        for (int k = 0; k < x.pieces; k += 4) {
-                            float f[4];
-                            float4 v[4][4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float* sl = slot_of(min(k + u, x.pieces - 1));
-                                f[u] = k + u < x.pieces ? __ldcg(sl + BM * kHeadDim + rr) : kNegInf;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) v[u][q] = __ldcg(reinterpret_cast<const float4*>(sl + rr * kHeadDim + c + 4 * q));
-                            }
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if (k + u >= x.pieces) break;
-                                const float fk = weight(f[u], ml.x);
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    o[q] = make_float4(o[q].x + fk * v[u][q].x, o[q].y + fk * v[u][q].y, o[q].z + fk * v[u][q].z,
-                                                       o[q].w + fk * v[u][q].w);
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) finish_row<PREFIX>(p, y, c + 4 * q, o[q], ml.x, ml.y);
-                    }
-                    if (row == 0) atomicExch(p.counters + x.c_first, 0u);
-                }
-                join_warps();
-            }
+            if (row == 0 && x.pieces > 1 && x.c_first == blockIdx.x)
+                p.shared[blockIdx.x] = SharedItem{x.pieces, x.b, x.e, x.rb, x.len, x.n_rows, {0, 0}};
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
         }
@@ -907,45 +852,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
 }
 
-// Joins the pieces of a prefix's items that several CTAs shared: sixteen threads per
-// row.  There is one sequence, of known length, so that the axis is the host's too.
-struct JoinParams {
-    PagedParams p;
-    int blocks[2], tiles, per, more;  // row blocks of a keyed entry and of the others
-    Divisor by_blocks[2];
-};
-__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinParams j) {
+// Joins the pieces of the items that several CTAs shared, in key order: eight
+// blocks per CTA of the launch before, sixteen threads per row.
+template <bool PREFIX>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
     griddep_launch_dependents();  // (what comes after reads nothing of this call's before it waits in turn)
     griddep_wait();
-    const PagedParams& p = j.p;
     constexpr int SLOT = BM * (kHeadDim + 2);
-    const int item = blockIdx.x >> 3, in_block = (blockIdx.x & 7) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
-    const int units_o = j.tiles * TcAxis::kUnit + TcAxis::kItem, units_r = j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem;
-    const int before = p.keyed * j.blocks[0];  // items of keyed entries
-    const int kind = item >= before, nth = kind ? item - before : item;  // (among the items of its kind)
-    const int e_nth = j.by_blocks[kind].div(nth), rb = nth - e_nth * j.blocks[kind], e = kind ? p.keyed + e_nth : e_nth;
-    const int start = kind ? before * units_o + nth * units_r : nth * units_o;
-    int first;
-    const int pieces = pieces_of(j.per, j.more, TcAxis::kItem, TcAxis::kSnap, start,
-                                 j.tiles * (kind ? TcAxis::kUnitKeyless : TcAxis::kUnit), first);
-    if (pieces == 1) return;
-    const RowInfo x = row_info<true>(p, 0, e, p.prefix_len, p.B * p.T, rb * BM + in_block);
+    const int first = blockIdx.x >> 3, in_block = (blockIdx.x & 7) * 16 + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    const SharedItem it = p.shared[first];
+    if (it.pieces == 0) return;
+    const RowInfo x = row_info<PREFIX>(p, it.b, it.e, it.len, it.n_rows, it.rb * BM + in_block);
     if (x.out < 0) return;
     auto slot_of = [&](int k) { return p.slots + ((size_t)(first + k) * 2 + (k == 0)) * SLOT; };
     float mm = kNegInf;
 #pragma unroll 8
-    for (int k = 0; k < pieces; ++k) mm = fmaxf(mm, slot_of(k)[BM * kHeadDim + in_block]);
+    for (int k = 0; k < it.pieces; ++k) mm = fmaxf(mm, slot_of(k)[BM * kHeadDim + in_block]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < pieces; ++k) {
+    for (int k = 0; k < it.pieces; ++k) {
         const float* sl = slot_of(k);
         const float f = weight(sl[BM * kHeadDim + in_block], mm);
         const float4 v = *reinterpret_cast<const float4*>(sl + in_block * kHeadDim + c);
         o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
         l += f * sl[BM * (kHeadDim + 1) + in_block];
     }
-    finish_row<true>(p, x, c, o, mm, l);
+    finish_row<PREFIX>(p, x, c, o, mm, l);
 }
 
 template <bool PREFIX>
@@ -978,23 +911,12 @@ cudaError_t launch(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) 
     launch_begin(kid, stream);
     e = cudaLaunchKernelEx(&cfg, paged_tc_kernel<PREFIX>, mk, mv, p);
     launch_end(kid, stream);
-    if (e != cudaSuccess || !PREFIX) return e != cudaSuccess ? e : cudaGetLastError();
-    JoinParams j;  // AxisWalk's own figures
-    j.p = p;
-    j.blocks[0] = (p.hp[0] * rows + BM - 1) / BM;
-    j.blocks[1] = (p.hp[1] * padded(rows, p.pad) + BM - 1) / BM;
-    for (int k = 0; k < 2; ++k) j.by_blocks[k] = divisor(j.blocks[k]);
-    const int items[2] = {p.keyed * j.blocks[0], (p.entries - p.keyed) * j.blocks[1]};
-    j.tiles = std::max(1, (p.prefix_len + BN - 1) / BN);
-    const int total = items[0] * (j.tiles * TcAxis::kUnit + TcAxis::kItem) + items[1] * (j.tiles * TcAxis::kUnitKeyless + TcAxis::kItem);
-    const int ctas = std::max(1, std::min(paged_grid(), total / TcAxis::kMinUnits));
-    j.per = total / ctas;
-    j.more = total - j.per * ctas;
-    cfg.gridDim = dim3((unsigned)((items[0] + items[1]) * 8));
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(paged_grid() * 8));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     launch_begin(KID_PAGED_JOIN, stream);
-    e = cudaLaunchKernelEx(&cfg, prefix_join_kernel, j);
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<PREFIX>, p);
     launch_end(KID_PAGED_JOIN, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
