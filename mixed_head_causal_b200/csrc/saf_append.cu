@@ -6,6 +6,10 @@
 // apart, in another lane of the group (exchanged by shuffles); interleaved
 // pairs (2i, 2i+1) lie inside a chunk.  Rows q, k, v of a token form one axis of
 // H + 2 H_kv rows.
+//
+// HBM bounds long appends: 8 x 4096 tokens of 12 heads (3 replaced), with the rotated
+// keys beside the cache, 290 MB in 60 us, 4.9 TB/s (44 us at a plain copy's rate).  A
+// step's few rows take 2 to 5 us, a launch's latency.
 #include <algorithm>
 
 #include "saf_paged.cuh"
@@ -155,8 +159,9 @@ cudaError_t launch_kv_append(AppendParams& p, cudaStream_t stream) {
     p.by_T = divisor(p.T);
     p.log_page = 0;
     while ((1 << p.log_page) < p.kv.page_size) ++p.log_page;
-    // few rows: one per eight lanes, for the most of them at once
-    return (int64_t)p.B * p.T * (p.H + 2 * p.kv.H_kv) < 16384 ? launch<1>(p, stream) : launch<4>(p, stream);
+    // Few rows: one per eight lanes, for the most of them at once.  With 1 and 4 rows of a token per eight lanes: 12,288
+    // rows 2.5 and 3.2 us, 25,200 3.1 and 3.5, 64,890 5.0 and 4.2, 1.2 million 85 and 58 (2: 73, 6 and 8: 65).
+    return (int64_t)p.B * p.T * (p.H + 2 * p.kv.H_kv) < 32768 ? launch<1>(p, stream) : launch<4>(p, stream);
 }
 
 }  // namespace saf

@@ -31,7 +31,14 @@
 //
 // One new token makes this a stream of K and V at a few flops per byte: HBM
 // bounds it, so the warp-level MMAs are enough, and the kernel is built for bytes
-// in flight and short chains.
+// in flight and short chains.  64 sequences of 16384 keys, 12 heads (3 replaced, no K):
+// 2.82 GB in 420 us, 6.7 TB/s (a plain copy's rate).  Short work shows the
+// latencies instead: 8 sequences of up to 4096 keys 18 us (10 at that rate), 512 keys
+// of one sequence 8.5 us; five drafted tokens of 32 sequences (four heads to a K/V
+// head: 20 rows, four warps for want of registers) 95 us against 52.
+// Rows on the M side, sixteen at least, would leave most of an MMA to padding: with the
+// keys there instead, 96 registers hold a warp's rows and eight warps fit (the first
+// of these shapes 515 -> 418 us).
 #include "mma_util.cuh"
 #include "saf_paged.cuh"
 
@@ -46,7 +53,6 @@ constexpr int CTAS_PER_SM = 2;
 struct SplitAxis {
     static constexpr int kTile = TK, kTileKeyless = 2 * TK, kUnit = 1, kUnitKeyless = 1, kItem = 4, kSnap = 4, kMinUnits = 8;
 };
-constexpr int kMaxBlocks = 4;        // row blocks of eight that one item holds
 constexpr uint32_t HALF = TK * 128;  // bytes of a tile's K or V
 constexpr uint32_t STAGE = 2 * HALF;
 constexpr int RED_PITCH = 68;        // floats per row of a warp's O: a warp's stores hit distinct banks
@@ -65,7 +71,7 @@ template <int NB>
 struct Smem {
     static constexpr int ROWS = 8 * NB;
     static constexpr int NCW = NB == 1 ? 8 : 4;                     // consumer warps (their registers: see KC)
-    static constexpr int NS = NB <= 2 ? 5 : NB == 3 ? 4 : 3;        // ring stages
+    static constexpr int NS = NB <= 2 ? 5 : 4;                      // ring stages
     static constexpr int NI = NB <= 2 ? 4 : 3;                      // items under way
     static constexpr int KC = NB <= 2 ? 64 : 32;                    // keys whose scores a warp holds at a time
     static constexpr uint32_t RED = NS * STAGE;                     // [NCW][ROWS][RED_PITCH] O of a warp
@@ -95,9 +101,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                    const __grid_constant__ PagedParams p) {
     using L = Smem<NB>;
     constexpr int ROWS = L::ROWS, NCW = L::NCW, NS = L::NS, NI = L::NI, KB = L::KC / 16, NCONS = 32 * NCW;
-    // P as one bf16 (half a step of 2^-8 off, as in the layer's own forward), or as a hi + lo pair of 16 bits where
-    // the second product is free: with up to eight rows the stream of K and V leaves the tensor pipe the room.
-    constexpr bool SPLIT_P = NB == 1;
+    // P is rounded to one bf16 (half a step of 2^-8 off, as in the layer's own forward): as a hi + lo pair the second
+    // product takes 20.0 us instead of 17.8 at 8 sequences of up to 4096 keys.
     constexpr int SLOT = ROWS * (kHeadDim + 2);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -430,7 +435,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     }
                 }
                 // P^T, rounded, turned into the second product's B fragments
-                uint32_t ph[KB][NB][2], pl[KB][NB][2];
+                uint32_t pt[KB][NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     // (x - m) * unit, not x * unit - m * unit: the products may overflow where the difference is small
@@ -443,14 +448,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                                 split_f32x2(mul_f32x2(sub_f32x2(f32x2(st[kb][nb][2 * u], st[kb][nb][2 * u + 1]), base2), unit2[nb]));
                             const float p0 = ex2(e.x), p1 = ex2(e.y);
                             l2[nb] = add_f32x2(l2[nb], f32x2(p0, p1));
-                            if (SPLIT_P) {
-                                uint32_t hi, lo;
-                                mma::pack_bf16_split(p0, p1, hi, lo);
-                                ph[kb][nb][u] = transpose8(hi);
-                                pl[kb][nb][u] = transpose8(lo);
-                            } else {
-                                ph[kb][nb][u] = transpose8(pack_bf16x2(p0, p1));
-                            }
+                            pt[kb][nb][u] = transpose8(pack_bf16x2(p0, p1));
                         }
                 }
 #pragma unroll
@@ -477,10 +475,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                             a[3] &= keep[1];
                         }
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            mma_bf16(o[d][nb], a, ph[kb][nb][0], ph[kb][nb][1]);
-                            if (SPLIT_P) mma_bf16(o[d][nb], a, pl[kb][nb][0], pl[kb][nb][1]);
-                        }
+                        for (int nb = 0; nb < NB; ++nb) mma_bf16(o[d][nb], a, pt[kb][nb][0], pt[kb][nb][1]);
                     }
                 }
             }
@@ -576,12 +571,11 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 }
 
 // ------------------------------------------------------------------ host side
-// Rows are dealt in blocks of up to 32, as even as eight allows.
-int row_blocks(int rows) { return (rows + 8 * kMaxBlocks - 1) / (8 * kMaxBlocks); }
-int block_rows(int rows) { return ((rows + row_blocks(rows) - 1) / row_blocks(rows) + 7) & ~7; }
-
-// Items of more rows than this go to the tensor-core kernel.
-constexpr int kTcRows = 32;
+// Items of more rows than this go to the tensor-core kernel.  Measured, this kernel's us against that one's: 16 rows (a
+// prefix of 2048 keys) 30 against 40, 24 of them 39 against 35; 20 rows (32 sequences of up to 8192 keys, 4 heads to a
+// K/V head) 95 against 185, 24 of them 101 against 187; 32 rows of the same two kinds 67 against 38, 200 against 193
+// (a fourth block of eight spills).
+constexpr int kTcRows = 24;
 
 // Workspace: header, the two launches' piece counters, shared items and pieces,
 // the prefix's parts.  Sizes grow with each argument.
@@ -638,15 +632,15 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
 template <bool PREFIX>
 cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, cudaStream_t stream) {
     p.pad = 1;
+    static_assert(kTcRows == 24, "three blocks of eight rows");
     make_entries(p, p.G, p.G, false);
-    p.block_rows = block_rows(PREFIX ? p.B * p.R : p.R);
+    p.block_rows = ((PREFIX ? p.B * p.R : p.R) + 7) & ~7;  // (all in one block)
     p.by_block = divisor(p.block_rows);
     if (!axis_fits<SplitAxis>(p, PREFIX)) return cudaErrorNotSupported;
     switch (p.block_rows / 8) {
         case 1: return launch_split<1, PREFIX>(mk, mv, p, stream);
         case 2: return launch_split<2, PREFIX>(mk, mv, p, stream);
-        case 3: return launch_split<3, PREFIX>(mk, mv, p, stream);
-        default: return launch_split<4, PREFIX>(mk, mv, p, stream);
+        default: return launch_split<3, PREFIX>(mk, mv, p, stream);
     }
 }
 

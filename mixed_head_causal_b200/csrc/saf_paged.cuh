@@ -105,8 +105,8 @@ struct PagedParams {
     unsigned int *err, *counters;
     float* slots;                // pieces: two per CTA
     SharedItem* shared;          // per CTA, of the tensor-core kernel
-    // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order K/V
-    // head (by order[]), head of the group, sequence, token.
+    // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order of
+    // heads[], sequence, token.
     float* part;
     int part_rows;
 };

@@ -36,6 +36,14 @@ def test_chunks_head_layouts(H, Hkv, T, replaced):
     run_attn(Cache([T + 2, 260, T], Hkv, 32, seed=H), H, T, [h in replaced for h in range(H)])
 
 
+@pytest.mark.parametrize("H,Hkv,T", [(256, 1, 1), (256, 256, 1), (256, 128, 20)])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_most_heads(H, Hkv, T, prefix):
+    """256 heads: of one K/V head, each its own, two to one; every third replaced, and the last group."""
+    mask = [int(h % 3 == 0 or h >= H - H // Hkv) for h in range(H)]
+    run_attn(Cache([T + 3], Hkv, 16, seed=H, prefix=prefix), H, T, mask)
+
+
 def test_chunk_bad_pages():
     c = Cache([200, 90, 140], 2, 16, seed=3)
     c.table[0, [0, 5, 12]] = [-1, c.kv.num_pages, -5]
