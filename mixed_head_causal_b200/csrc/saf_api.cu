@@ -78,11 +78,14 @@ saf_status check_paged_kv(const saf_paged_kv* kv, int H) {
     return SAF_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 // Page tables and lengths of B sequences (B > 0) of T new tokens each.
 saf_status check_tables(const saf_paged_kv& kv, const int32_t* page_table, int max_pages, const int32_t* seq_lens,
-                        int max_len) {
+                        const int32_t* q_lens, int max_len) {
     if (max_pages < 0 || max_len < 0 || max_len > (int64_t)max_pages * kv.page_size) return SAF_ERR_INVALID_ARG;
     if (!seq_lens || (max_len > 0 && !page_table)) return SAF_ERR_INVALID_ARG;
+    if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(q_lens)) return SAF_ERR_INVALID_ARG;
     return SAF_OK;
 }
 
@@ -386,7 +389,7 @@ saf_status saf_kv_append(const saf_paged_kv* kv, const void* q, const int64_t* q
     st = check_paged_kv(kv, H);
     if (st != SAF_OK) return st;
     if ((int64_t)B * H * T == 0) return SAF_OK;
-    st = check_tables(*kv, page_table, max_pages, seq_lens, max_len);
+    st = check_tables(*kv, page_table, max_pages, seq_lens, q_lens, max_len);
     if (st != SAF_OK) return st;
     if (!k || !v || !aligned16(k) || !aligned16(v) || (q == nullptr) != (q_out == nullptr)) return SAF_ERR_INVALID_ARG;
     if ((q && (!aligned16(q) || !aligned16(q_out))) || (k_out && !aligned16(k_out))) return SAF_ERR_INVALID_ARG;
@@ -442,10 +445,10 @@ saf_status saf_paged_attn_prefix(const saf_paged_kv* kv, const void* q, void* o,
     if (st != SAF_OK) return st;
     if (prefix_len < 0) return SAF_ERR_INVALID_ARG;
     if ((int64_t)B * H * T_q == 0) return SAF_OK;
-    st = check_tables(*kv, page_table, max_pages, seq_lens, max_len);
+    st = check_tables(*kv, page_table, max_pages, seq_lens, q_lens, max_len);
     if (st != SAF_OK) return st;
     if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return SAF_ERR_INVALID_ARG;
-    if (prefix_len > 0 && !prefix_table) return SAF_ERR_INVALID_ARG;
+    if (prefix_len > 0 && (!prefix_table || !aligned4(prefix_table))) return SAF_ERR_INVALID_ARG;
     // positions, and rows of one K/V head over the batch, in 32 bits
     if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || (int64_t)B * H * T_q > INT_MAX / 128) return SAF_ERR_INVALID_ARG;
     PagedCall p{};

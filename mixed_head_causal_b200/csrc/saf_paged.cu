@@ -33,7 +33,7 @@
 // bounds it, so the warp-level MMAs are enough, and the kernel is built for bytes
 // in flight and short chains.  64 sequences of 16384 keys, 12 heads (3 replaced, no K):
 // 2.82 GB in 420 us, 6.7 TB/s (a plain copy's rate).  Short work shows the
-// latencies instead: 8 sequences of up to 4096 keys 18 us (10 at that rate), 512 keys
+// latencies instead: 8 sequences of up to 4096 keys 24 us (10 at that rate), 512 keys
 // of one sequence 8.5 us; five drafted tokens of 32 sequences (four heads to a K/V
 // head: 20 rows, four warps for want of registers) 95 us against 52.
 // Rows on the M side, sixteen at least, would leave most of an MMA to padding: with the
@@ -102,7 +102,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     using L = Smem<NB>;
     constexpr int ROWS = L::ROWS, NCW = L::NCW, NS = L::NS, NI = L::NI, KB = L::KC / 16, NCONS = 32 * NCW;
     // P is rounded to one bf16 (half a step of 2^-8 off, as in the layer's own forward): as a hi + lo pair the second
-    // product takes 20.0 us instead of 17.8 at 8 sequences of up to 4096 keys.
+    // product takes 20.0 us instead of 17.8 at 8 sequences of up to 4096 keys that are in L2.
     constexpr int SLOT = ROWS * (kHeadDim + 2);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -379,6 +379,8 @@ def _check_serving(name, t, dtype, shape, device) -> int:
 def _check_tables(kv, page_table, seq_lens, q_lens, B, max_len):
     """(page_table, max_pages, seq_lens, q_lens, max_len) for the library."""
     device, cols = kv.device, page_table.shape[-1]
+    if max_len is not None and not 0 <= max_len <= cols * kv.page_size:
+        raise ValueError(f"max_len {max_len}: the page table holds {cols * kv.page_size} positions")
     return (_check_serving("page_table", page_table, torch.int32, (B, cols), device), cols,
             _check_serving("seq_lens", seq_lens, torch.int32, (B,), device),
             None if q_lens is None else _check_serving("q_lens", q_lens, torch.int32, (B,), device),
@@ -468,6 +470,8 @@ def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, kv: P
 def _kv_append(kv, q, k, v, page_table, seq_lens, mask, q_lens, rope, interleaved, max_len, pos_offset, q_out, k_out, H):
     B, Hkv, T, _ = k.shape
     device = kv.device
+    if not 0 <= pos_offset <= 0x7fffffff:
+        raise ValueError("pos_offset out of range")
     if Hkv != kv.h_kv:
         raise ValueError(f"k has {Hkv} heads, the cache {kv.h_kv}")
     if mask is not None:
@@ -558,7 +562,8 @@ def paged_attn(q, kv: PagedKV, page_table, seq_lens, alpha=None, rho=None, mask=
     are device tensors, read by the kernels; max_len bounds the lengths.  mask,
     alpha, rho: the replaced heads and their pattern ([H, pattern_len], at least
     max_len long).  Callers that run many steps pass out, lse and a workspace
-    (new_paged_workspace)."""
+    (new_paged_workspace).  No gradient is kept: a cache is not trained through
+    (the layer's own backward is mixed_attn_bwd)."""
     return _paged(kv, stream, q, None, 0, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse, workspace)
 
 
@@ -569,8 +574,8 @@ def paged_attn_prefix(q, kv: PagedKV, prefix_table, prefix_len: int, page_table,
     """paged_attn for a batch whose sequences all begin with the same
     prefix_len tokens, cached once in the pages prefix_table [ceil(prefix_len /
     page_size)]: the other arguments describe what follows the prefix."""
-    if prefix_len < 0:
-        raise ValueError("prefix_len < 0")
+    if not 0 <= prefix_len <= 0x7fffffff:
+        raise ValueError("prefix_len out of range")
     return _paged(kv, stream, q, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
                   workspace)
 

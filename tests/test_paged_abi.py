@@ -66,7 +66,7 @@ def test_cache_refusals(lib, call):
 def test_table_refusals(lib, call):
     bad = saf.SAF_ERR_INVALID_ARG
     for kw in [dict(table=None), dict(seq=None), dict(max_pages=-1), dict(max_len=65), dict(max_len=-1), dict(B=-1), dict(T=-1),
-               dict(q=None), dict(q=FAKE + 2)]:
+               dict(q=None), dict(q=FAKE + 2), dict(table=FAKE + 2), dict(seq=FAKE + 1), dict(ql=FAKE + 2)]:
         assert call(lib, **kw) == bad, kw
     assert call(lib, H=300, cache=kv(H_kv=300)) == saf.SAF_ERR_UNSUPPORTED
 
@@ -96,7 +96,7 @@ def test_attention_refusals(lib):
     bad = saf.SAF_ERR_INVALID_ARG
     for kw in [dict(o=None), dict(lse=None), dict(o=FAKE + 2), dict(a=None), dict(r=None), dict(a=FAKE + 4), dict(plen=63)]:
         assert attn(lib, **kw) == bad, kw
-    for kw in [dict(ptab=None), dict(pre=-1), dict(plen=103)]:
+    for kw in [dict(ptab=None), dict(ptab=FAKE + 2), dict(pre=-1), dict(plen=103)]:
         assert attn(lib, prefix=True, **kw) == bad, kw
     assert attn(lib, ws=None) == saf.SAF_ERR_WORKSPACE
     assert attn(lib, wsb=saf.paged_workspace_size(2, 4, 1, 2) - 1) == saf.SAF_ERR_WORKSPACE
