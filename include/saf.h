@@ -363,8 +363,9 @@ SAF_API saf_status saf_kv_append(const saf_paged_kv *kv,
  *            replaced head pattern_len >= max_len.
  *   workspace  at least saf_paged_workspace_size(B,H,H_kv,T_q,0) bytes, 256-byte
  *            aligned, of the serving calls alone: zeroed once before first use
- *            (every call leaves its counters zero again), not shared with the
- *            layer's entry points, and not used by two calls at once.
+ *            (every call leaves its counters zero again; after a call that
+ *            saf_device_status reports as failed, zero it once more), not shared
+ *            with the layer's entry points, and not used by two calls at once.
  * Slots at or past a sequence's length may hold anything, NaN included.  A V
  * value that one row of a call sees must be finite if another row of the same
  * sequence must not see it (T_q > 1): a hidden key has weight zero, and zero
