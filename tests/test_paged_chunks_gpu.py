@@ -52,6 +52,24 @@ def test_chunk_bad_pages():
     run_attn(c, 4, 40, [0, 1, 0, 0])
 
 
+@pytest.mark.parametrize("T,prefix,lens", [(1, 0, [300, 9, 64]), (5, 0, [300, 9, 64]), (40, 0, [300, 41, 64]),
+                                           (1, 139, [1 + 31 * i for i in range(40)]), (2, 139, [2 + i for i in range(40)])])
+def test_unused_pattern_entries_are_not_read(T, prefix, lens):
+    """NaN in the rows of ordinary heads and behind the longest position."""
+    c = Cache(lens, 2, 16, seed=3, prefix=prefix)
+    n = prefix + max(lens)
+    a, r = pattern(4, n + 13, torch.Generator().manual_seed(5))
+    for x in (a, r):
+        x[:, n:] = float("nan")
+        x[[0, 2]] = float("nan")
+    run_attn(c, 4, T, [0, 1, 0, 1], a=a, r=r)
+
+
+def test_thousands_of_sequences():
+    g = np.random.default_rng(2)
+    run_attn(Cache([int(n) for n in g.integers(0, 40, 4100)], 1, 16, seed=6, prefix=33), 1, 1, [0])
+
+
 def test_chunk_infinite_patterns():
     c = Cache([150, 64, 300], 2, 16, seed=3)
     a, r = pattern(4, 300, torch.Generator().manual_seed(5))
