@@ -349,6 +349,16 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             if (!ok && lane == 0) report(p.err, 0x402);
             const uint32_t bad = meta[s] >> (sub ? TK >> lb : 0);
             const bool whole = k0 + TK <= x.vmin && bad == 0;  // every row sees every key
+            if (!whole) {  // a slot without a token may hold a NaN, and 0 times that is one: its V becomes zeros
+#pragma unroll 1
+                for (int j = lane; j < TK; j += 32) {
+                    if (k0 + j < x.len && !((bad >> (j >> lb)) & 1u)) continue;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) st_shared_v4(sv + 128 * j + 16 * ((c + lane) & 7), 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();  // (before the stage's next load)
+                __syncwarp();
+            }
 #pragma unroll
             for (int kc = 0; kc < TK; kc += L::KC) {
                 float st[KB][NB][4];
@@ -386,13 +396,23 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (!whole) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
-                        const int v0 = info[nb * 8 + r0].vis, v1 = info[nb * 8 + r0 + 1].vis;
+                        // this thread's keys are kb * 16 + 8 * (e >> 1) past the first of them
+                        const int first = k0 + kc + (lane >> 2), v0 = info[nb * 8 + r0].vis - first, v1 = info[nb * 8 + r0 + 1].vis - first;
 #pragma unroll
                         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int jl = kc + kb * 16 + (lane >> 2) + 8 * (e >> 1);
-                                if (k0 + jl >= ((e & 1) ? v1 : v0) || ((bad >> (jl >> lb)) & 1u)) st[kb][nb][e] = kNegInf;
+                            for (int e = 0; e < 4; ++e)
+                                if (kb * 16 + 8 * (e >> 1) >= ((e & 1) ? v1 : v0)) st[kb][nb][e] = kNegInf;
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int jl = kc + kb * 16 + (lane >> 2) + 8 * u;
+                                if (!((bad >> (jl >> lb)) & 1u)) continue;
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) st[kb][nb][2 * u] = st[kb][nb][2 * u + 1] = kNegInf;
                             }
                     }
                 }
@@ -453,27 +473,12 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    uint32_t keep[2] = {~0u, ~0u};
-                    if (!whole) {  // a slot without a token may hold a NaN, and 0 times that is one
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int jl = kc + kb * 16 + 8 * u + r0, j = k0 + jl;
-                            const bool dead = (bad >> (jl >> lb)) & 1u;
-                            keep[u] = dead ? 0u : (j < x.len ? 0xffffu : 0u) | (j + 1 < x.len ? 0xffff0000u : 0u);
-                        }
-                    }
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
                         // V^T: 16 columns x 16 keys, from V stored [key][column]
                         uint32_t a[4];
                         const int key = kc + kb * 16 + (lane & 7) + (lane >> 4) * 8, col = d * 16 + ((lane >> 3) & 1) * 8;
                         mma::ldsm_x4_t(a[0], a[1], a[2], a[3], sv + mma::swz(key, col));
-                        if (!whole) {
-                            a[0] &= keep[0];
-                            a[1] &= keep[0];
-                            a[2] &= keep[1];
-                            a[3] &= keep[1];
-                        }
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) mma_bf16(o[d][nb], a, pt[kb][nb][0], pt[kb][nb][1]);
                     }
