@@ -35,7 +35,7 @@
 // 2.82 GB in 420 us, 6.7 TB/s (a plain copy's rate).  Short work shows the
 // latencies instead: 8 sequences of up to 4096 keys 24 us (10 at that rate), 512 keys
 // of one sequence 8.5 us; five drafted tokens of 32 sequences (four heads to a K/V
-// head: 20 rows, four warps for want of registers) 95 us against 52.
+// head: 20 rows, four warps for want of registers) 98 us against 52.
 // Rows on the M side, sixteen at least, would leave most of an MMA to padding: with the
 // keys there instead, 96 registers hold a warp's rows and eight warps fit (the first
 // of these shapes 515 -> 418 us).
@@ -353,7 +353,9 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll 1
                 for (int j = lane; j < TK; j += 32) {
                     if (k0 + j < x.len && !((bad >> (j >> lb)) & 1u)) continue;
-#pragma unroll
+                    // a row per lane, the lanes' 16 bytes in distinct banks (unrolled where there are registers: 20 rows
+                    // lose 13 us of 97 to spills otherwise)
+#pragma unroll(NB == 1 ? 8 : 1)
                     for (int c = 0; c < 8; ++c) st_shared_v4(sv + 128 * j + 16 * ((c + lane) & 7), 0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();  // (before the stage's next load)
