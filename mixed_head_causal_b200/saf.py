@@ -573,9 +573,12 @@ def paged_attn_prefix(q, kv: PagedKV, prefix_table, prefix_len: int, page_table,
                       stream=None):
     """paged_attn for a batch whose sequences all begin with the same
     prefix_len tokens, cached once in the pages prefix_table [ceil(prefix_len /
-    page_size)]: the other arguments describe what follows the prefix."""
+    page_size)] (so many entries exactly; a longer table is sliced): the other
+    arguments describe what follows the prefix."""
     if not 0 <= prefix_len <= 0x7fffffff:
         raise ValueError("prefix_len out of range")
+    if prefix_table is None and prefix_len:
+        raise ValueError("prefix_table: a prefix needs its pages")
     return _paged(kv, stream, q, prefix_table, prefix_len, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse,
                   workspace)
 

@@ -129,3 +129,8 @@ def test_binding_refuses_host_tensors():
     k = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="k_cache"):
         saf.PagedKV(k, k)
+
+
+def test_binding_refuses_a_prefix_without_pages():
+    with pytest.raises(ValueError, match="prefix_table"):
+        saf.paged_attn_prefix(None, None, None, 20, None, None)
