@@ -392,6 +392,8 @@ class _Guards:
     it allocates belongs to the stream it runs on."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:     # (its kernels would run on the other device's memory)
+            raise ValueError(f"stream: a stream of {stream.device}, the cache or table is on {device}")
         self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

@@ -1,6 +1,7 @@
 """Refusals of the serving entry points, on the host: every call here fails
 its argument checks (or is empty) before anything is enqueued."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -134,3 +135,18 @@ def test_binding_refuses_host_tensors():
 def test_binding_refuses_a_prefix_without_pages():
     with pytest.raises(ValueError, match="prefix_table"):
         saf.paged_attn_prefix(None, None, None, 20, None, None)
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    cache = SimpleNamespace(device=torch.device("cuda", 0))
+    other = SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        saf.paged_attn(None, cache, None, None, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        saf.paged_attn_prefix(None, cache, torch.zeros(2), 20, None, None, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        saf.kv_append(None, None, None, cache, None, None, n_heads=1, stream=other)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: SimpleNamespace(device=torch.device("cuda", 0)))
+    with pytest.raises(ValueError, match="stream"):
+        saf.rope_table(4, stream=other)
