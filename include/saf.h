@@ -366,6 +366,14 @@ SAF_API saf_status saf_kv_append(const saf_paged_kv *kv,
  *            (every call leaves its counters zero again; after a call that
  *            saf_device_status reports as failed, zero it once more), not shared
  *            with the layer's entry points, and not used by two calls at once.
+ * Limits: B * H * T_q and max_len (with a prefix prefix_len + max_len) are at
+ * most 2^31 - 4097, else SAF_ERR_INVALID_ARG (saf_paged_workspace_size:
+ * (size_t)-1).  The work of the longest lengths allowed, whatever the lengths
+ * are, is counted in 31 bits, else SAF_ERR_UNSUPPORTED.  With n sequences of L
+ * keys and T rows a head (the prefix: n = 1, L = prefix_len, T = B * T_q; what
+ * follows it: n = B, L = max_len, T = T_q) that is n H_kv (L / 64 + 5) units where
+ * T * H / H_kv <= 24, else n H (T / 128 + 1) (L / 32 + 8) at most; up to 2.1e9 of
+ * them are taken.
  * Slots at or past a sequence's length may hold anything, NaN included.  A V
  * value that one row of a call sees must be finite if another row of the same
  * sequence must not see it (T_q > 1): a hidden key has weight zero, and zero

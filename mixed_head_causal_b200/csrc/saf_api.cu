@@ -78,6 +78,9 @@ saf_status check_paged_kv(const saf_paged_kv* kv, int H) {
     return SAF_OK;
 }
 
+// Rows of an attention call: the kernels count them in 31 bits, some padding included.
+bool rows_fit(int B, int H, int T) { return (int64_t)B * H * T <= INT_MAX - 4096; }
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // Page tables and lengths of B sequences (B > 0) of T new tokens each.
@@ -427,7 +430,8 @@ saf_status saf_kv_append(const saf_paged_kv* kv, const void* q, const int64_t* q
 }
 
 size_t saf_paged_workspace_size(int B, int H, int H_kv, int T_q, int prefix_len) {
-    if (check_shape(B, H, T_q, kHeadDim) != SAF_OK || check_groups(H, H_kv) != SAF_OK || prefix_len < 0)
+    if (check_shape(B, H, T_q, kHeadDim) != SAF_OK || check_groups(H, H_kv) != SAF_OK || prefix_len < 0 ||
+        !rows_fit(B, H, T_q))
         return (size_t)-1;
     if ((int64_t)B * H * T_q == 0) return 0;
     return paged_workspace_bytes(B, H, H_kv, T_q, prefix_len);
@@ -449,8 +453,8 @@ saf_status saf_paged_attn_prefix(const saf_paged_kv* kv, const void* q, void* o,
     if (st != SAF_OK) return st;
     if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return SAF_ERR_INVALID_ARG;
     if (prefix_len > 0 && (!prefix_table || !aligned4(prefix_table))) return SAF_ERR_INVALID_ARG;
-    // positions, and rows of one K/V head over the batch, in 32 bits
-    if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || (int64_t)B * H * T_q > INT_MAX / 128) return SAF_ERR_INVALID_ARG;
+    // positions, and rows, in 31 bits
+    if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || !rows_fit(B, H, T_q)) return SAF_ERR_INVALID_ARG;
     PagedCall p{};
     p.replaced = head_bits(replaced_mask, H);
     p.keyless = keyless_bits(p.replaced, H, kv->H_kv);

@@ -385,13 +385,18 @@ inline bool make_tmap_pages(const saf_paged_kv& kv, bool keys, int max_rows, CUt
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks and units of the longest possible axis must fit 31 bits.
+// The rows of an entry and the units of the longest axis must fit 31 bits, with room for a stretch's length and padding.
 template <class A>
 bool axis_fits(const PagedParams& p, bool prefix) {
-    const double rows = (double)std::max(p.hp[0], p.hp[1]) * ((prefix ? (double)p.B * p.T : (double)p.T) + p.pad - 1);
-    const double blocks = rows / p.block_rows + 1;
-    const double most = A::kItem + A::kUnitKeyless * std::max(1.0, (double)(prefix ? p.prefix_len : p.max_len) / A::kTile + 1);
-    return rows < 2147483648.0 - 256 && most * blocks * p.entries * p.nseq < 2147483648.0;
+    const int64_t n = prefix ? (int64_t)p.B * p.T : p.T, keys = prefix ? p.prefix_len : p.max_len;
+    double units = 0;
+    for (int keyless = 0; keyless < 2; ++keyless) {
+        const int64_t rows = p.hp[keyless] * (keyless ? (n + p.pad - 1) / p.pad * p.pad : n), tile = keyless ? A::kTileKeyless : A::kTile;
+        if (rows > INT_MAX - 256) return false;
+        const double item = A::kItem + (double)std::max<int64_t>(1, (keys + tile - 1) / tile) * (keyless ? A::kUnitKeyless : A::kUnit);
+        units += item * (double)((rows + p.block_rows - 1) / p.block_rows) * (keyless ? p.entries - p.keyed : p.keyed);
+    }
+    return units * p.nseq <= 2147483648.0 - (1 << 24);
 }
 // Entries of up to hp heads of one K/V head each, hp_replaced where none of them is ordinary; apart: of one kind each.
 inline void make_entries(PagedParams& p, int hp, int hp_replaced, bool apart) {

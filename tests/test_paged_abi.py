@@ -150,3 +150,18 @@ def test_binding_refuses_a_stream_of_another_device(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *a, **kw: SimpleNamespace(device=torch.device("cuda", 0)))
     with pytest.raises(ValueError, match="stream"):
         saf.rope_table(4, stream=other)
+
+
+def test_row_limit(lib):
+    """Rows of a call are counted in 31 bits: a size below is wanted a workspace of, one past is refused by both calls."""
+    bad, none = saf.SAF_ERR_INVALID_ARG, ctypes.c_size_t(-1).value
+    for B, H, T in ((64, 4, 8192 * 8), (127, 4, 1 << 22)):
+        assert attn(lib, B=B, H=H, T=T, wsb=0) == saf.SAF_ERR_WORKSPACE
+        assert attn(lib, prefix=True, B=B, H=H, T=T, wsb=0) == saf.SAF_ERR_WORKSPACE
+        rows = B * H * T
+        assert rows * 66 * 4 < lib.saf_paged_workspace_size(B, H, 2, T, 40) < rows * 66 * 4 + (1 << 26)
+    assert attn(lib, B=128, H=4, T=1 << 22, wsb=0) == bad
+    assert attn(lib, prefix=True, B=128, H=4, T=1 << 22, wsb=0) == bad
+    assert lib.saf_paged_workspace_size(128, 4, 2, 1 << 22, 0) == none
+    assert lib.saf_paged_workspace_size(1, 256, 1, (1 << 25) - 1, 0) == none     # (256 times that is a multiple of 2^32, less 256)
+    assert lib.saf_paged_workspace_size(1, 256, 1, 1 << 24, 40) == none

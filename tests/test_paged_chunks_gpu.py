@@ -164,6 +164,50 @@ def test_no_new_tokens(T, B, prefix):
     assert saf.device_status(ws) == saf.SAF_OK
 
 
+@pytest.mark.parametrize("prefix", [0, 20])
+def test_rows_past_24_bits(prefix):
+    """64 sequences of 8192 new tokens and 32 heads, all but the last of them before position 0."""
+    B, H, Hkv, T, n = 64, 32, 8, 8192, 40
+    mask = [int(h % 5 == 0) for h in range(H)]
+    c = Cache([n] * B, Hkv, 16, seed=7, prefix=prefix)
+    table, seq = c.gpu()
+    a, r = pattern(H, prefix + n, torch.Generator().manual_seed(5))
+    q = torch.zeros(B, H, T, 64, dtype=torch.bfloat16, device="cuda")
+    some = prefix + n       # rows of a head that see a key
+    q[:, :, -some:] = torch.randn(B, H, some, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    kw = dict(alpha=a.cuda(), rho=r.cuda(), mask=mask, max_len=n)
+    ws = saf.new_paged_workspace(c.kv, B, H, T, prefix)
+    if prefix:
+        o, lse = saf.paged_attn_prefix(q, c.kv, torch.from_numpy(c.prefix_table).cuda(), prefix, table, seq, workspace=ws, **kw)
+    else:
+        o, lse = saf.paged_attn(q, c.kv, table, seq, workspace=ws, **kw)
+    assert saf.device_status(ws) == saf.SAF_OK
+    assert (o[:, :, :-some] == 0).all() and (lse[:, :, :-some] == -math.inf).all()
+    for b in (0, 31, 63):
+        ref = O.attend(np64(q[b:b + 1, :, -some:]), np64(c.k), np64(c.v), c.table[b:b + 1], [n], None, np64(a), np64(r), mask,
+                       n, c.prefix_table, prefix)
+        check(o[b:b + 1, :, -some:], lse[b:b + 1, :, -some:], ref, None, some)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_axis_limit(T):
+    """The longest lengths that max_len allows bound the work: below 31 bits short sequences run, past them the call is refused."""
+    page, H, max_len = 256, 2, 2 ** 31 - 2 ** 16
+    c = Cache([300, 45], H, page, seed=2)
+    q = torch.randn(40, H, T, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    table = torch.full((40, max_len // page), -1, dtype=torch.int32, device="cuda")
+    table[:2, :c.table.shape[1]] = c.gpu()[0]
+    seq = ints(c.lens + [0] * 38)
+    B = 20 if T == 1 else 12     # 33.5 million tiles of 64 keys; blocks of 128 count twice
+    o, lse = saf.paged_attn(q[:B].cuda(), c.kv, table[:B], seq[:B], max_len=max_len)
+    ref = O.attend(np64(q[:B]), np64(c.k), np64(c.v), np.pad(c.table, ((0, B - 2), (0, 0))), c.lens + [0] * (B - 2), None, None, None,
+                   [0] * H, 300)
+    check(o, lse, ref, None, T)
+    with pytest.raises(saf.SafError) as e:
+        saf.paged_attn(q.cuda(), c.kv, table, seq, max_len=max_len)
+    assert e.value.status == saf.SAF_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ together
 def test_prefill_by_chunks_matches_the_layer():
     """A prompt appended and attended chunk by chunk, ragged last chunks included: the layer's own rows."""
