@@ -430,6 +430,16 @@ SAF_API saf_status saf_device_status(void *workspace, size_t workspace_bytes, vo
 SAF_API saf_status saf_selftest_wait_timeout(void *workspace, size_t workspace_bytes, long long limit_cycles,
                                              void *stream);
 
+/*
+ * Failure-path self-test of the paged attention calls: their kernels' waits give
+ * up after limit_cycles SM cycles (1 .. 2^31; 0: the default, 2^31, about a
+ * second) in calls enqueued from now on by this process.  A wait that gives up
+ * ends its CTA's work, after what the CTA has in flight, and records the time-out
+ * in the call's workspace; outputs are then undefined, and the workspace is zeroed
+ * before its next use.
+ */
+SAF_API saf_status saf_selftest_serving_wait_limit(long long limit_cycles);
+
 /* ------------------------------------------------------------------------
  * Launch accounting and per-kernel timing (for benchmarks and tracing).
  * ------------------------------------------------------------------------ */

@@ -496,6 +496,12 @@ saf_status saf_paged_attn(const saf_paged_kv* kv, const void* q, void* o, float*
                                  seq_lens, q_lens, B, H, T_q, max_len, workspace, workspace_bytes, stream);
 }
 
+saf_status saf_selftest_serving_wait_limit(long long limit_cycles) {
+    if (limit_cycles < 0 || limit_cycles > kServingWaitLimit) return SAF_ERR_INVALID_ARG;
+    set_serving_wait_limit(limit_cycles);
+    return SAF_OK;
+}
+
 saf_status saf_selftest_wait_timeout(void* workspace, size_t workspace_bytes, long long limit_cycles,
                                      void* stream) {
     if (!workspace || workspace_bytes < sizeof(WsHeader)) return SAF_ERR_WORKSPACE;

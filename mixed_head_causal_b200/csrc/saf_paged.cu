@@ -39,6 +39,8 @@
 // Rows on the M side, sixteen at least, would leave most of an MMA to padding: with the
 // keys there instead, 96 registers hold a warp's rows and eight warps fit (the first
 // of these shapes 515 -> 418 us).
+#include <atomic>
+
 #include "mma_util.cuh"
 #include "saf_paged.cuh"
 
@@ -57,7 +59,6 @@ constexpr uint32_t HALF = TK * 128;  // bytes of a tile's K or V
 constexpr uint32_t STAGE = 2 * HALF;
 constexpr int RED_PITCH = 68;        // floats per row of a warp's O: a warp's stores hit distinct banks
 constexpr int Q_PITCH = 144;         // bytes per query row in shared memory: eight rows' words hit distinct banks
-constexpr long long kWaitLimit = 1ll << 31;
 
 // What the consumers need of an item's stretch: tiles [t0, t1), pieces of the
 // item in all, the CTA of its first one; vmin: keys that every row sees; replaced:
@@ -140,15 +141,9 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         AxisWalk<SplitAxis, PREFIX> walk(p, blockIdx.x, gridDim.x);
         const int lp = p.log_page, lb = min(lp, 6);  // page and box rows
         const uint32_t box_bytes = 128u << lb;
-        int it = 0;
-        // a wait gave up: the loads in flight land (or give up in turn) before the shared memory is let go
-        auto give_up = [&](unsigned code) {
-            if (lane == 0) {
-                report(p.err, code);
-                for (int k = max(0, it - NS); k < it; ++k) mbar_wait(bar_full + 8 * (k % NS), (k / NS) & 1, kWaitLimit);
-            }
-        };
-        for (int ni = 0;; ++ni) {
+        int it = 0, ni = 0;  // tiles whose loads have been issued, items whose queries have
+        unsigned gave_up = 0;
+        for (; !gave_up; ++ni) {
             Piece x;
             Stretch w;
             x.t1 = -1;  // no more
@@ -161,18 +156,16 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 x.c_first = w.c_first;
             }
             const int slot = ni % NI;
-            if (!mbar_wait_warp(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1, kWaitLimit)) {
-                give_up(0x403);
-                return;
+            if (!mbar_wait_warp(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1, p.wait_limit)) {
+                gave_up = 0x403;
+                break;
             }
             if (x.t1 < 0) {
                 if (lane == 0) {
                     reinterpret_cast<Piece*>(smem + L::ITEM + 48 * slot)->t1 = -1;
                     mbar_arrive(bar_item + 8 * slot);
                 }
-                // A grid in which none has waited may end before the one ahead of it, and the next would start too soon.
-                if (!PREFIX && p.part) griddep_wait();
-                return;
+                break;
             }
             const int g = p.e_g[w.e], row0 = w.rb * ROWS;
             x.rows = min(ROWS, max(0, p.e_heads[w.e] * w.n_rows - row0));
@@ -208,9 +201,9 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 const bool good = need && page >= 0 && page < p.num_pages;
                 const uint32_t bad = __ballot_sync(~0u, need && !good);
                 const int loads = __popc(__ballot_sync(~0u, good));
-                if (!mbar_wait_warp(bar_empty + 8 * s, ((it / NS) & 1) ^ 1, kWaitLimit)) {
-                    give_up(0x401);
-                    return;
+                if (!mbar_wait_warp(bar_empty + 8 * s, ((it / NS) & 1) ^ 1, p.wait_limit)) {
+                    gave_up = 0x401;
+                    break;
                 }
                 if (lane == 0) {
                     meta[s] = bad;
@@ -226,6 +219,16 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 if (lane == 0) *issued = it + 1;
             }
         }
+        if (gave_up && lane == 0) report(p.err, gave_up);
+        if (lane == 0) {  // the loads in flight land before the shared memory is let go, whether a consumer still wants them or not
+            for (int k = max(0, it - NS); k < it; ++k) mbar_wait(bar_full + 8 * (k % NS), (k / NS) & 1, kDrainLimit);
+            // (the mark of the end stands in the place of item ni - NI, which the consumers have taken)
+            for (int k = max(0, gave_up ? ni - NI : ni - NI + 1); k < ni; ++k)
+                mbar_wait(bar_item + 8 * (k % NI), (k / NI) & 1, kDrainLimit);
+        }
+        // A grid in which none has waited may end before the one ahead of it, and the next would start too soon.
+        if (!PREFIX && p.part) griddep_wait();
+        return;
     }
 
     // ---------------------------------------------------- consumers
@@ -242,14 +245,14 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     auto join_warps = [&] {
         mbar_arrive_warp(bar_join);
         if (ok) {
-            ok = mbar_wait_warp(bar_join, joins & 1, kWaitLimit);
+            ok = mbar_wait_warp(bar_join, joins & 1, p.wait_limit);
             if (!ok && lane == 0) report(p.err, 0x405);
         }
         ++joins;
     };
     for (int ni = 0;; ++ni) {
         if (ok) {
-            ok = mbar_wait_warp(bar_item + 8 * (ni % NI), (ni / NI) & 1, kWaitLimit);
+            ok = mbar_wait_warp(bar_item + 8 * (ni % NI), (ni / NI) & 1, p.wait_limit);
             if (!ok && lane == 0) report(p.err, 0x404);
         }
         const Piece x = *reinterpret_cast<const Piece*>(smem + L::ITEM + 48 * (ni % NI));
@@ -342,10 +345,10 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             // tile, the stage's fill before has been used up, and its barrier's parity can only tell of this one.
             if (ok && *issued <= (int)at) {
                 const long long began = clock64();
-                while (*issued <= (int)at && ok) ok = clock64() - began < kWaitLimit;
+                while (*issued <= (int)at && ok) ok = clock64() - began < p.wait_limit;
             }
             ok = __all_sync(~0u, ok);
-            if (ok) ok = mbar_wait_warp(bar_full + 8 * s, (at / NS) & 1, kWaitLimit);
+            if (ok) ok = mbar_wait_warp(bar_full + 8 * s, (at / NS) & 1, p.wait_limit);
             if (!ok && lane == 0) report(p.err, 0x402);
             const uint32_t bad = meta[s] >> (sub ? TK >> lb : 0);
             const bool whole = k0 + TK <= x.vmin && bad == 0;  // every row sees every key
@@ -487,7 +490,8 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_n(bar_empty + 8 * s, x.keyed ? 2 : 1);
+            // (a stage that this warp has given up on may still be landing, and is not filled again)
+            if (lane == 0 && ok) mbar_arrive_n(bar_empty + 8 * s, x.keyed ? 2 : 1);
         }
         it += x.t1 - x.t0;
 
@@ -657,6 +661,11 @@ size_t paged_workspace_bytes(int B, int H, int H_kv, int T, int prefix_len) {
     return paged_ws(B, H, H_kv, T, prefix_len).total;
 }
 
+namespace {
+std::atomic<long long> g_wait_limit{kServingWaitLimit};
+}
+void set_serving_wait_limit(long long cycles) { g_wait_limit = cycles ? cycles : kServingWaitLimit; }
+
 cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     CUtensorMap mk, mv;
     if (!make_tmap_pages(c.kv, true, TK, &mk) || !make_tmap_pages(c.kv, false, TK, &mv)) return cudaErrorNotSupported;
@@ -688,6 +697,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.by_T = divisor(p.T);
     p.by_BT = p.by_BT_pad = divisor(p.B * p.T);
     p.err = reinterpret_cast<unsigned int*>(c.ws);
+    p.wait_limit = g_wait_limit;
     if (c.prefix_len > 0) {
         p.part = reinterpret_cast<float*>(c.ws + w.part);
         p.part_rows = c.B * c.H * c.T;

@@ -103,6 +103,7 @@ struct PagedParams {
     uint8_t heads[kMaxHeads];    // query heads group by group, the ordinary ones of a group first
     Divisor by_T, by_BT, by_BT_pad, by_block;
     unsigned int *err, *counters;
+    long long wait_limit;        // cycles after which a wait gives up
     float* slots;                // pieces: two per CTA
     SharedItem* shared;          // per CTA, of the tensor-core kernel
     // What the prefix came to (or null): [part_rows][64] O, then m, then l, before the division; rows in the order of
@@ -110,6 +111,10 @@ struct PagedParams {
     float* part;
     int part_rows;
 };
+
+// Every wait on a barrier is bounded by PagedParams::wait_limit (about a second, see saf_selftest_serving_wait_limit);
+// a role that gave up waits, by this bound, for what it has under way itself before the memory is let go.
+constexpr long long kDrainLimit = 1ll << 31;
 
 __device__ __forceinline__ void report(unsigned int* err, unsigned int code) {
     atomicOr(err, 1u);
@@ -419,6 +424,9 @@ inline void make_entries(PagedParams& p, int hp, int hp_replaced, bool apart) {
         if (want == 0) p.keyed = p.entries;
     }
 }
+constexpr long long kServingWaitLimit = 1ll << 31;  // about a second
+void set_serving_wait_limit(long long cycles);      // 0: that
+
 // CTAs of either kernel, two per SM; bounds the workspace (pieces: two per CTA).
 constexpr int kMaxGrid = 320;
 inline int paged_grid() { return std::min(kMaxGrid, 2 * sm_count()); }

@@ -48,7 +48,6 @@ constexpr int NTHREADS = 192;
 constexpr uint32_t TILE_BYTES = 128 * 64 * 2;
 constexpr uint32_t TMEM_COLS = 256;
 constexpr uint32_t TO_COL = 128, TP_COL = 192;  // S in 0..127, O, P
-constexpr long long kWaitLimit = 1ll << 31;
 
 // shared memory map (offsets from a 1024-aligned base)
 constexpr uint32_t SM_Q = 0;
@@ -68,7 +67,8 @@ constexpr uint32_t SM_BAR = SM_ROW + 128 * 8;
 constexpr uint32_t SM_ITEM = SM_BAR + 20 * 8;       // [2] TcPiece
 constexpr uint32_t SM_WARP = SM_ITEM + 2 * 48;      // [4] WarpRows
 constexpr uint32_t SM_MISC = SM_WARP + 4 * 80;      // TMEM address, [4] boxes of a K load without a page, [4] of a V load
-constexpr uint32_t SM_TOTAL = SM_MISC + 40;
+constexpr uint32_t SM_LIMIT = SM_MISC + 40;         // PagedParams::wait_limit, for the row loops
+constexpr uint32_t SM_TOTAL = SM_LIMIT + 8;
 
 struct TcAxis {
     // (a block of replaced rows takes about twice as long as one of ordinary rows: 3.6 us against 1.8, two CTAs per SM)
@@ -113,6 +113,16 @@ __device__ __forceinline__ const volatile TcPiece& item_of(int ni) {
     return reinterpret_cast<volatile TcPiece*>(smem_base() + SM_ITEM)[ni & 1];
 }
 __device__ __forceinline__ const WarpRows& warp_rows() { return reinterpret_cast<WarpRows*>(smem_base() + SM_WARP)[quarter_of()]; }
+// A wait of the row loops (mbar_wait_warp, the limit looked up only where there is something to wait for).
+__device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const long long began = clock64();
+        do ok = mbar_try_wait(bar, parity);
+        while (!ok && clock64() - began <= *reinterpret_cast<const volatile long long*>(smem_base() + SM_LIMIT));
+    }
+    return __all_sync(~0u, ok);
+}
 __device__ __forceinline__ float* staging() { return reinterpret_cast<float*>(smem_base() + SM_PAT + quarter_of() * PAT_BYTES); }
 
 // The values of a TMEM load pass through here once the load has been waited for, so
@@ -396,10 +406,10 @@ __device__ __forceinline__ bool block_arrived(bool keyed, int nk, int nv, uint32
     if (keyed) {
         // (not the K stage's barrier: it may be a fill ahead by now; what the producer wrote before the load was
         // seen by the MMA warp before it issued S)
-        ok = mbar_wait_warp(sbase + BAR_S, nk & 1, kWaitLimit);
+        ok = row_wait(sbase + BAR_S, nk & 1);
         bad = ld_shared_u32(sbase + SM_KMETA + 4 * (nk & 3));
     } else {
-        ok = mbar_wait_warp(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+        ok = row_wait(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1);
         bad = ld_shared_u32(sbase + SM_VMETA + 4 * (nv & 3));
     }
     tc_fence_after();
@@ -408,7 +418,7 @@ __device__ __forceinline__ bool block_arrived(bool keyed, int nk, int nv, uint32
 // P V of the block before has read P and added to O (an item's first: waited for by the item before).
 __device__ __forceinline__ bool p_free(bool first, int nv) {
     if (first) return true;
-    const bool ok = mbar_wait_warp(smem_addr(smem_base()) + BAR_O, (nv - 1) & 1, kWaitLimit);
+    const bool ok = row_wait(smem_addr(smem_base()) + BAR_O, (nv - 1) & 1);
     tc_fence_after();
     return ok;
 }
@@ -428,7 +438,7 @@ __device__ __forceinline__ bool clear_dead(int ni, int nv, int k0, uint32_t bad)
     if (k0 + BN <= len && !bad) return true;
     const uint32_t sbase = smem_addr(smem_base());
     const int row = quarter_of() * 32 + (threadIdx.x & 31);
-    const bool ok = mbar_wait_warp(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1, kWaitLimit);
+    const bool ok = row_wait(sbase + BAR_VF + 8 * (nv & 1), (nv >> 1) & 1);
     if (k0 + row >= len || ((bad >> (row >> item_of(ni).lb)) & 1u)) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) st_shared_v4(sbase + SM_V + (nv & 1) * TILE_BYTES + row * 128 + 16 * c, 0, 0, 0, 0);
@@ -579,6 +589,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         mbar_init(bar_sf, 4);
         mbar_init(bar_p, 4);
         mbar_init(bar_o, 1);
+        *reinterpret_cast<long long*>(smem + SM_LIMIT) = p.wait_limit;
         fence_mbar_init();
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -630,7 +641,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 x.nt = max(0, min(w.t1, (most + BN - 1) / BN) - w.t0);
             }
             const int slot = ni & 1;
-            ok = mbar_wait_warp(bar_taken + 8 * slot, ((ni >> 1) & 1) ^ 1, kWaitLimit);
+            ok = mbar_wait_warp(bar_taken + 8 * slot, ((ni >> 1) & 1) ^ 1, p.wait_limit);
             if (!ok) break;
             if (lane == 0) {
                 items[slot] = x;
@@ -656,7 +667,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const bool good = need && page >= 0 && page < p.num_pages;
                 const uint32_t bad = __ballot_sync(~0u, lane < boxes && !good);
                 const int loads = __popc(__ballot_sync(~0u, good));
-                if (!mbar_wait_warp(empty, ((at >> 1) & 1) ^ 1, kWaitLimit)) {
+                if (!mbar_wait_warp(empty, ((at >> 1) & 1) ^ 1, p.wait_limit)) {
                     --(keys ? nk : nv);
                     return false;
                 }
@@ -678,10 +689,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 if (ok) ok = load(i, false);
             }
         }
-        if (!ok && lane == 0) {  // a wait gave up: the loads in flight land (or give up in turn) before the memory is let go
-            report(p.err, 0x501);
-            for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
-            for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kWaitLimit);
+        if (!ok && lane == 0) report(p.err, 0x501);
+        if (lane == 0) {  // the loads in flight land before the shared memory is let go, whether anyone still wants them or not
+            for (int i = max(0, nk - 2); i < nk; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, kDrainLimit);
+            for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, kDrainLimit);
         }
         // A grid in which none has waited may end before the one ahead of it, and the next would start too soon.
         if (!PREFIX && p.part) griddep_wait();
@@ -694,7 +705,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         int nk = 0, nv = 0, nq = 0;  // S and P V products issued, items with queries
         bool ok = true;
         for (int ni = 0; ok; ++ni) {
-            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
+            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, p.wait_limit);
             if (!ok) break;
             const int nt = items[ni & 1].nt;
             const bool keyed = items[ni & 1].keyed && nt > 0;
@@ -704,8 +715,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             auto issue_s = [&] {
                 const int s = nk & 1;
                 // the rows have copied the S before (an item's first: that item's last)
-                if (nk > 0 && !mbar_wait_warp(bar_sf, (nk - 1) & 1, kWaitLimit)) return false;
-                if (!mbar_wait_warp(bar_kf + 8 * s, (nk >> 1) & 1, kWaitLimit)) return false;
+                if (nk > 0 && !mbar_wait_warp(bar_sf, (nk - 1) & 1, p.wait_limit)) return false;
+                if (!mbar_wait_warp(bar_kf + 8 * s, (nk >> 1) & 1, p.wait_limit)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -719,13 +730,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 return true;
             };
             if (keyed) {
-                ok = mbar_wait_warp(bar_q, nq & 1, kWaitLimit) && issue_s();
+                ok = mbar_wait_warp(bar_q, nq & 1, p.wait_limit) && issue_s();
                 ++nq;
             }
             for (int i = 0; ok && i < nt; ++i) {
                 if (keyed && i + 1 < nt) ok = issue_s();
                 const int s = nv & 1;
-                ok = ok && mbar_wait_warp(bar_vf + 8 * s, (nv >> 1) & 1, kWaitLimit) && mbar_wait_warp(bar_p, nv & 1, kWaitLimit);
+                ok = ok && mbar_wait_warp(bar_vf + 8 * s, (nv >> 1) & 1, p.wait_limit) && mbar_wait_warp(bar_p, nv & 1, p.wait_limit);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -740,6 +751,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
         }
         if (!ok && lane == 0) report(p.err, 0x502);
+        // the products in flight end before the operands and TMEM are let go, whether the rows still want them or not
+        if (nk > 0) mbar_wait_warp(bar_s, (nk - 1) & 1, kDrainLimit);
+        if (nv > 0) mbar_wait_warp(bar_o, (nv - 1) & 1, kDrainLimit);
     } else {
         // ------------------------------------------------ row threads
         const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -748,7 +762,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         bool ok = true, waited = false;
         if (row == 0) p.shared[blockIdx.x].pieces = 0;  // until there is one
         for (int ni = 0; ok; ++ni) {
-            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, kWaitLimit);
+            ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, p.wait_limit);
             if (!ok) break;
             const TcPiece x = items[ni & 1];
             if (x.nt < 0) break;
@@ -811,7 +825,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             nv += x.nt;
             if (keyed) nk += x.nt;
             const float m = rep ? res.m : 0.125f * res.m, l = res.l;
-            if (ok && x.nt > 0) ok = mbar_wait_warp(bar_o, (nv - 1) & 1, kWaitLimit);
+            if (ok && x.nt > 0) ok = mbar_wait_warp(bar_o, (nv - 1) & 1, p.wait_limit);
             tc_fence_after();
             if (!ok) break;
             if (!PREFIX && p.part && !waited) {
@@ -849,7 +863,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_taken + 8 * (ni & 1));
         }
-        if (!ok && lane == 0) report(p.err, 0x503);
+        if (!ok) {
+            if (lane == 0) report(p.err, 0x503);
+            tmem_wait_st();
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -37,6 +37,7 @@ SIGNATURES = {
     "saf_mixed_attn_bwd_gqa": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                 _vp, _vp, _vp, _i, _vp, _sz, _vp], _i),
     "saf_device_status": ([_vp, _sz, _vp], _i),
+    "saf_selftest_serving_wait_limit": ([ctypes.c_longlong], _i),
     "saf_selftest_wait_timeout": ([_vp, _sz, ctypes.c_longlong, _vp], _i),
     "saf_replaced_pattern_grad": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp], _i),
     "saf_calibration_workspace_size": ([_i, _i, _i], _sz),
@@ -596,6 +597,12 @@ def selftest_wait_timeout(workspace: torch.Tensor, limit_cycles: int = 1 << 20, 
     workspace's error word when it gives up; see device_status)."""
     _check(load().saf_selftest_wait_timeout(_ptr(workspace), workspace.numel() * workspace.element_size(),
                                             int(limit_cycles), _stream_ptr(stream)), "saf_selftest_wait_timeout")
+
+
+def selftest_serving_wait_limit(limit_cycles: int = 0) -> None:
+    """Bounds the waits of paged attention calls made from now on (0: the
+    default): a test's way to make one give up (see device_status)."""
+    _check(load().saf_selftest_serving_wait_limit(int(limit_cycles)), "saf_selftest_serving_wait_limit")
 
 
 def launch_count() -> int:
