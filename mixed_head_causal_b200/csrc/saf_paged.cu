@@ -143,6 +143,17 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         const uint32_t box_bytes = 128u << lb;
         int it = 0, ni = 0;  // tiles whose loads have been issued, items whose queries have
         unsigned gave_up = 0;
+        // What the producer waits for comes from warps that stop for a prefix's launch before they leave their first
+        // item, for as long as it takes.  Past that item it awaits that launch itself, once there is something to wait
+        // for, and only then is the wait bounded.
+        bool behind = !PREFIX && p.part;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (behind && ni > 0 && !__all_sync(~0u, mbar_try_wait(bar, parity))) {
+                griddep_wait();
+                behind = false;
+            }
+            return mbar_wait_warp(bar, parity, p.wait_limit);
+        };
         for (; !gave_up; ++ni) {
             Piece x;
             Stretch w;
@@ -156,7 +167,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 x.c_first = w.c_first;
             }
             const int slot = ni % NI;
-            if (!mbar_wait_warp(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1, p.wait_limit)) {
+            if (!wait(bar_taken + 8 * slot, ((ni / NI) & 1) ^ 1)) {
                 gave_up = 0x403;
                 break;
             }
@@ -201,7 +212,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 const bool good = need && page >= 0 && page < p.num_pages;
                 const uint32_t bad = __ballot_sync(~0u, need && !good);
                 const int loads = __popc(__ballot_sync(~0u, good));
-                if (!mbar_wait_warp(bar_empty + 8 * s, ((it / NS) & 1) ^ 1, p.wait_limit)) {
+                if (!wait(bar_empty + 8 * s, ((it / NS) & 1) ^ 1)) {
                     gave_up = 0x401;
                     break;
                 }

@@ -616,6 +616,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         int nk = 0, nv = 0;  // K and V loads so far
         bool ok = true;
         for (int ni = 0; ok; ++ni) {
+            // The rows stop for a prefix's launch before they leave their first item, for as long as it takes: past that
+            // item no bounded wait for them (or, by way of them, for the MMA warp) begins before it has ended.
+            if (!PREFIX && p.part && ni == 1) griddep_wait();
             Stretch w;
             TcPiece x;
             x.nt = -1;
@@ -705,6 +708,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         int nk = 0, nv = 0, nq = 0;  // S and P V products issued, items with queries
         bool ok = true;
         for (int ni = 0; ok; ++ni) {
+            if (!PREFIX && p.part && ni == 1) griddep_wait();  // (as the producer does)
             ok = mbar_wait_warp(bar_item + 8 * (ni & 1), (ni >> 1) & 1, p.wait_limit);
             if (!ok) break;
             const int nt = items[ni & 1].nt;
@@ -752,8 +756,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         if (!ok && lane == 0) report(p.err, 0x502);
         // the products in flight end before the operands and TMEM are let go, whether the rows still want them or not
-        if (nk > 0) mbar_wait_warp(bar_s, (nk - 1) & 1, kDrainLimit);
-        if (nv > 0) mbar_wait_warp(bar_o, (nv - 1) & 1, kDrainLimit);
+        if (lane == 0 && nk > 0) mbar_wait(bar_s, (nk - 1) & 1, kDrainLimit);
+        if (lane == 0 && nv > 0) mbar_wait(bar_o, (nv - 1) & 1, kDrainLimit);
     } else {
         // ------------------------------------------------ row threads
         const int quarter = warp & 3, row = quarter * 32 + lane;

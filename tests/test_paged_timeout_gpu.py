@@ -77,3 +77,30 @@ def test_nothing_waits_for_the_limit(T):
     end.synchronize()
     assert begin.elapsed_time(end) < 300        # milliseconds; the limit is a second
     assert saf.device_status(ws) == saf.SAF_OK
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (28, 1)], ids=["few_rows", "tensor_core"])
+def test_the_prefix_may_take_longer_than_the_limit(wait_limit, H, Hkv):
+    """Lengths far apart, so that the prefix's replaced rows, each with its own stretch of r, take longer than the
+    axis gives them: the CTAs that are through first go on to the sequences' own keys, and wait for the others for a
+    few times the limit (25 us; a wait inside either launch is for a few us, an item's end for 15)."""
+    B, T, mask, prefix = 128, 1, [int(2 * h >= H) for h in range(H)], 1 << 20
+    g = torch.Generator().manual_seed(1)
+    lens = [T + int(n) for n in torch.randint(0, 3000, (B,), generator=g)]
+    c = Cache(lens, Hkv, 64, seed=3, prefix=640)
+    table, seq = c.gpu()
+    pages = torch.from_numpy(c.prefix_table).cuda().repeat(prefix // 640 + 1)[:prefix // 64].contiguous()   # the same ten over and over
+    a, r = (x.cuda() for x in pattern(H, prefix + max(lens), g))
+    q = torch.randn(B, H, T, 64, generator=g).bfloat16().cuda()
+    ws = saf.new_paged_workspace(c.kv, B, H, T, prefix)
+
+    def call():
+        return saf.paged_attn_prefix(q, c.kv, pages, prefix, table, seq, alpha=a, rho=r, mask=mask, max_len=max(lens), workspace=ws)
+
+    want = [x.clone() for x in call()]
+    assert saf.device_status(ws) == saf.SAF_OK
+    wait_limit(48_000)
+    for _ in range(3):
+        got = call()
+        assert saf.device_status(ws) == saf.SAF_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
