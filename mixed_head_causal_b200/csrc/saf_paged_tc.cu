@@ -94,7 +94,7 @@ struct WarpRows {
     int pure;              // all rows with a token look up, by one head's vectors
     int low, span;         // from r on: the lowest of their stretches, and from there to the highest
     int low_edge;          // the 16-byte boundary at or before the lowest's entry of local key 127
-    int room, before;      // floats of the array from r on, and before it (2^30 at most)
+    int room, before;      // floats of the array from r on (2^31 - 9 at most), and before it (2^31 - 1 at most)
     int last;              // the last key
     int vmin;              // keys that every row sees
 };
@@ -249,8 +249,9 @@ __device__ __forceinline__ void near_copy(int k0) {
     // from the boundary at or before the lowest row's last key to the highest row's first key
     const int edge = w.low_edge, stop = w.low + w.span + 1;
     for (int at = edge + 4 * lane; at < stop; at += 128) {
-        const bool in = at - k0 + w.before >= 0;
-        const int bytes = in ? min(4, w.room + k0 - at) * 4 : 0;  // (the last may reach past the array)
+        const int rel = at - k0;  // (sums of these stay within 31 bits: positions come near that far)
+        const bool in = rel >= -w.before;
+        const int bytes = in ? min(4, w.room - max(rel, -4)) * 4 : 0;  // (the last may reach past the array)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(buf + (128 + at - edge) * 4),
                      "l"(in ? r + at : w.r0), "r"(bytes));
     }
@@ -295,7 +296,7 @@ __device__ __forceinline__ void far_copy(int edge, int key) {  // the 16 keys fr
         const uint32_t dst = buf + (i < 4 ? (8 * i + (lane >> 2)) * FAR_PITCH + 4 * (lane & 3) : lane * FAR_PITCH + 16) * 4;
         const int src = i < 4 ? __shfl_sync(~0u, edge, 8 * i + (lane >> 2)) + 4 * (lane & 3) : edge + 16;
         // the fifth may end past the array's last float, or begin there (a stretch that starts on a boundary needs none)
-        const int bytes = i < 4 ? 16 : min(4, max(0, w.room + key - src)) * 4;
+        const int bytes = i < 4 ? 16 : min(4, max(0, w.room - max(src - key, -4))) * 4;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(r + src), "r"(bytes));
     }
     if (lane < 16) copy4(buf + (FAR_A + lane) * 4, a + lane);
@@ -812,8 +813,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 w.low = low;
                 w.low_edge = (int)(((r_first + low - 127) & ~3ll) - r_first);
                 w.span = span;
-                w.room = (int)min((long long)p.H * p.pattern_len - r_first, 1ll << 30);
-                w.before = (int)min(r_first, 1ll << 30);
+                w.room = (int)min((long long)p.H * p.pattern_len - r_first, (long long)INT_MAX - 8);
+                w.before = (int)min(r_first, (long long)INT_MAX);
                 w.last = max(x.len, 1) - 1;
                 w.vmin = vmin;
             }

@@ -208,6 +208,51 @@ def test_axis_limit(T):
     assert e.value.status == saf.SAF_ERR_UNSUPPORTED
 
 
+BASE = 2 ** 30
+
+
+@pytest.mark.parametrize("H,T,prefix,lens", [
+    (1, 1, 0, [BASE + 300]), (2, 64, 0, [BASE + 300]),                      # one row, a chunk
+    (1, 1, BASE, [300 + 37 * b for b in range(40)]), (2, 2, BASE, [300 + 37 * b for b in range(20)]),
+    (1, 1, 256, [10 + b + BASE * (b % 2) for b in range(40)]),              # rows that far apart
+])
+def test_positions_past_30_bits(H, T, prefix, lens):
+    """2^30 keys and more, the same pages over and over, under replaced heads whose pattern (two arrays of 4 GB a head)
+    leaves weight near a row's own position alone: the fp64 formula over the last keys."""
+    page, near, B = 256, 2000, len(lens)
+    g = torch.Generator().manual_seed(B)
+    kc, vc = (torch.randn(16, H, page, 64, generator=g).bfloat16() for _ in range(2))
+    kv = saf.PagedKV(kc.cuda(), vc.cuda())
+    n, cols = prefix + max(lens), -(-max(lens) // page)
+    on_gpu = torch.Generator(device="cuda").manual_seed(1)
+    pages = torch.randint(0, 16, (prefix // page,), generator=on_gpu, device="cuda", dtype=torch.int32)
+    table = torch.randint(0, 16, (B, cols), generator=on_gpu, device="cuda", dtype=torch.int32)
+    r = (torch.arange(n, device="cuda", dtype=torch.float32) * -0.05).repeat(H, 1)
+    a = 0.5 * torch.randn(H, n, generator=on_gpu, device="cuda")
+    q = torch.zeros(B, H, T, 64, dtype=torch.bfloat16, device="cuda")
+    kw = dict(alpha=a, rho=r, mask=[1] * H, max_len=max(lens))
+    if prefix:
+        o, lse = saf.paged_attn_prefix(q, kv, pages, prefix, table, ints(lens), **kw)
+    else:
+        o, lse = saf.paged_attn(q, kv, table, ints(lens), **kw)
+    v64 = np64(vc)
+    for b in range(B):
+        for t in range(T):
+            i = prefix + lens[b] - T + t
+            j = torch.arange(max(0, i - near), i + 1, device="cuda")
+            at = torch.where(j < prefix, pages[torch.clamp(j // page, max=prefix // page - 1)] if prefix else 0,
+                             table[b][torch.clamp(j - prefix, min=0) // page]).cpu().numpy()
+            slot = (torch.where(j < prefix, j, j - prefix) % page).cpu().numpy()
+            for h in range(H):
+                v = v64[at, h, slot]
+                s = np64(a[h, j]) - 0.05 * np64(i - j)
+                w = np.exp(s - s.max())
+                want, total = w @ v / w.sum(), s.max() + np.log(w.sum())
+                bound = U16 * np.abs(want) + (U16 + 2 * S_TOL) * (w @ np.abs(v) / w.sum())
+                assert (np.abs(np64(o[b, h, t]) - want) <= bound).all(), (b, h, t)
+                assert abs(float(lse[b, h, t]) - total) <= S_TOL + 2 * U32 * abs(total)
+
+
 # ------------------------------------------------------------------ together
 def test_prefill_by_chunks_matches_the_layer():
     """A prompt appended and attended chunk by chunk, ragged last chunks included: the layer's own rows."""
