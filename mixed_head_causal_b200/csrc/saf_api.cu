@@ -457,7 +457,6 @@ saf_status saf_paged_attn_prefix(const saf_paged_kv* kv, const void* q, void* o,
     if ((int64_t)prefix_len + max_len > INT_MAX - 4096 || !rows_fit(B, H, T_q)) return SAF_ERR_INVALID_ARG;
     PagedCall p{};
     p.replaced = head_bits(replaced_mask, H);
-    p.keyless = keyless_bits(p.replaced, H, kv->H_kv);
     bool any = false;
     for (uint32_t w : p.replaced.w) any |= w != 0;
     if (any) {

@@ -652,7 +652,9 @@ cudaError_t launch_split(const CUtensorMap& mk, const CUtensorMap& mv, const Pag
 }
 
 template <bool PREFIX>
-cudaError_t launch_split_rows(const CUtensorMap& mk, const CUtensorMap& mv, PagedParams& p, cudaStream_t stream) {
+cudaError_t launch_split_rows(const saf_paged_kv& kv, PagedParams& p, cudaStream_t stream) {
+    CUtensorMap mk, mv;
+    if (!make_tmap_pages(kv, true, TK, &mk) || !make_tmap_pages(kv, false, TK, &mv)) return cudaErrorNotSupported;
     p.pad = 1;
     static_assert(kTcRows == 24, "three blocks of eight rows");
     make_entries(p, p.G, p.G, false);
@@ -678,8 +680,6 @@ std::atomic<long long> g_wait_limit{kServingWaitLimit};
 void set_serving_wait_limit(long long cycles) { g_wait_limit = cycles ? cycles : kServingWaitLimit; }
 
 cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
-    CUtensorMap mk, mv;
-    if (!make_tmap_pages(c.kv, true, TK, &mk) || !make_tmap_pages(c.kv, false, TK, &mv)) return cudaErrorNotSupported;
     const PagedWs w = paged_ws(c.B, c.H, c.kv.H_kv, c.T, c.prefix_len);
     PagedParams p{};
     p.q = c.q;
@@ -719,7 +719,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
         p.slots = reinterpret_cast<float*>(c.ws + w.slots[1]);
         p.shared = reinterpret_cast<SharedItem*>(c.ws + w.shared[1]);
         const cudaError_t e = c.B * p.R > kTcRows ? launch_paged_tc(c.kv, p, true, stream)
-                                               : launch_split_rows<true>(mk, mv, p, stream);
+                                               : launch_split_rows<true>(c.kv, p, stream);
         if (e != cudaSuccess) return e;
     }
     p.table = c.page_table;
@@ -728,7 +728,7 @@ cudaError_t launch_paged_attn(const PagedCall& c, cudaStream_t stream) {
     p.counters = reinterpret_cast<unsigned int*>(c.ws + w.counters[0]);
     p.slots = reinterpret_cast<float*>(c.ws + w.slots[0]);
     p.shared = reinterpret_cast<SharedItem*>(c.ws + w.shared[0]);
-    if (p.R <= kTcRows) return launch_split_rows<false>(mk, mv, p, stream);
+    if (p.R <= kTcRows) return launch_split_rows<false>(c.kv, p, stream);
     return launch_paged_tc(c.kv, p, false, stream);
 }
 

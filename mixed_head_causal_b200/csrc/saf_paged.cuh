@@ -59,7 +59,6 @@ struct PagedCall {
     const float *a, *r;
     int pattern_len;
     HeadBits replaced;   // per query head
-    HeadBits keyless;    // per K/V head: all its query heads are replaced
     const int32_t* prefix_table;
     int prefix_len;
     const int32_t *page_table, *seq_lens, *q_lens;
