@@ -177,6 +177,16 @@ __device__ __forceinline__ RowInfo row_info(const PagedParams& p, int b, int e, 
     x.out = (rb * p.H + h) * p.T + t;
     x.part = (hs * p.B + rb) * p.T + t;
     x.replaced = p.replaced.get(h) ? h + 1 : 0;
+    // (the index-checked build) its entries of a and r, the output's row and the part's
+    [[maybe_unused]] const long long entries = (long long)p.H * p.pattern_len;
+    if (!SAF_CHECKED_OK(p.err,
+                        x.out >= 0 && x.out < p.B * p.H * p.T && x.part >= 0 && x.part < p.B * p.H * p.T &&
+                            (!x.replaced || x.vis == 0 ||
+                             (x.a0 >= 0 && x.a0 + x.vis <= entries && x.r0 < entries && x.r0 - x.vis + 1 >= 0)),
+                        0x9401u)) {
+        x.out = -1;
+        x.vis = x.replaced = 0;
+    }
     return x;
 }
 
@@ -353,7 +363,12 @@ struct AxisWalk {
         x.pieces = pieces_of(per, more, A::kItem, A::kSnap, start, x.n * w, x.c_first);
         u = start + A::kItem + x.n * w;  // (or past the stretch)
         if (u > end) u = end;
-        return true;
+        // (the index-checked build) the item, its tiles within the keys that the table holds, its pieces' slots
+        return SAF_CHECKED_OK(p.err,
+                              b >= 0 && b < p.nseq && x.e >= 0 && x.e < p.entries && x.rb >= 0 && x.t0 >= 0 && x.t0 <= x.t1 &&
+                                  x.t1 <= x.n && len <= (PREFIX ? p.prefix_len : p.max_len) && x.pieces >= 1 &&
+                                  (x.pieces == 1 || (x.c_first >= 0 && x.c_first + x.pieces <= ctas)),
+                              0x9402u);
     }
 };
 
