@@ -30,10 +30,6 @@ __global__ void rope_table_kernel(float* table, int max_pos, int rot_dim, double
     }
 }
 
-// Two bf16 as a pair of fp32.
-__device__ __forceinline__ uint64_t pair_of(uint32_t w) {
-    return tc::f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
 // x cos + y sin of a pair, rounded to bf16 (the products and their sum in fp32).
 __device__ __forceinline__ uint32_t turn(uint32_t x, uint32_t y, uint64_t cs, uint64_t sn) {
     const float2 v = tc::split_f32x2(tc::fma_f32x2(pair_of(x), cs, tc::mul_f32x2(pair_of(y), sn)));

@@ -102,8 +102,11 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                    const __grid_constant__ PagedParams p) {
     using L = Smem<NB>;
     constexpr int ROWS = L::ROWS, NCW = L::NCW, NS = L::NS, NI = L::NI, KB = L::KC / 16, NCONS = 32 * NCW;
-    // P is rounded to one bf16 (half a step of 2^-8 off, as in the layer's own forward): as a hi + lo pair the second
-    // product takes 20.0 us instead of 17.8 at 8 sequences of up to 4096 keys that are in L2.
+    // P is rounded to one bf16 (half a step of 2^-8 off): as a hi + lo pair the second product takes 20.0 us instead of
+    // 17.8 at 8 sequences of up to 4096 keys that are in L2 (416 instead of 413 at 64 of 16384).  O is divided by the sum
+    // of the rounded weights, as the layer's forward divides a replaced head's: what all keys have in common comes
+    // out exactly, and a dominant key's V is not scaled by its weight's rounding.  l, which lse and the joins
+    // go by, is the sum of the weights before they are rounded.
     constexpr int SLOT = ROWS * (kHeadDim + 2);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,7 +287,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         // Running maximum (in units of the row's scores: dot products for an ordinary row), its log2(e) per unit, the sum
         // (of this thread's keys) and O^T (columns 16 db + lane / 4, + 8), for this thread's two rows of each block.
         float m[NB][2], o[4][NB][4];
-        uint64_t unit2[NB], l2[NB];
+        uint64_t unit2[NB], l2[NB], lr2[NB];  // lr2: the sum of the rounded weights
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             float un[2];
@@ -294,7 +297,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 un[e] = ((x.replaced >> (nb * 8 + r0 + e)) & 1u) ? kLog2e : 0.125f * kLog2e;
             }
             unit2[nb] = f32x2(un[0], un[1]);
-            l2[nb] = 0;
+            l2[nb] = lr2[nb] = 0;
 #pragma unroll
             for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -464,6 +467,7 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                             if (up) m[nb][e] = v;
                         }
                         l2[nb] = mul_f32x2(l2[nb], f32x2(f[0], f[1]));
+                        lr2[nb] = mul_f32x2(lr2[nb], f32x2(f[0], f[1]));
 #pragma unroll
                         for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -484,7 +488,9 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                                 split_f32x2(mul_f32x2(sub_f32x2(f32x2(st[kb][nb][2 * u], st[kb][nb][2 * u + 1]), base2), unit2[nb]));
                             const float p0 = ex2(e.x), p1 = ex2(e.y);
                             l2[nb] = add_f32x2(l2[nb], f32x2(p0, p1));
-                            pt[kb][nb][u] = transpose8(pack_bf16x2(p0, p1));
+                            const uint32_t pr = pack_bf16x2(p0, p1);
+                            lr2[nb] = add_f32x2(lr2[nb], pair_of(pr));
+                            pt[kb][nb][u] = transpose8(pr);
                         }
                 }
 #pragma unroll
@@ -509,21 +515,25 @@ paged_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         // ---- the warps' parts to shared memory, joined over the keys
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float2 ll = split_f32x2(l2[nb]);
+            const float2 ll = split_f32x2(l2[nb]), lr = split_f32x2(lr2[nb]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = nb * 8 + r0 + e;
-                float l = e ? ll.y : ll.x;
+                float l = e ? ll.y : ll.x, rounded = e ? lr.y : lr.x;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
+                for (int d = 4; d < 32; d <<= 1) {
+                    l += __shfl_xor_sync(~0u, l, d);
+                    rounded += __shfl_xor_sync(~0u, rounded, d);
+                }
+                const float f = by_rounded(l, rounded);
                 if (lane < 4) {
                     red_m[warp * ROWS + row] = ((x.replaced >> row) & 1u) ? m[nb][e] : 0.125f * m[nb][e];
                     red_l[warp * ROWS + row] = l;
                 }
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    mine[row * RED_PITCH + d * 16 + (lane >> 2)] = o[d][nb][e];
-                    mine[row * RED_PITCH + d * 16 + (lane >> 2) + 8] = o[d][nb][2 + e];
+                    mine[row * RED_PITCH + d * 16 + (lane >> 2)] = o[d][nb][e] * f;
+                    mine[row * RED_PITCH + d * 16 + (lane >> 2) + 8] = o[d][nb][2 + e] * f;
                 }
             }
         }

@@ -128,6 +128,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
+// Two bf16 as a pair of fp32.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) {
+    return tc::f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// What takes an O of rounded weights, whose sum is `rounded`, to the sum l of the weights themselves.
+__device__ __forceinline__ float by_rounded(float l, float rounded) { return rounded > 0.f ? __fdividef(l, rounded) : 1.f; }
 // exp(x - m) for finite or -inf x <= m (m = -inf: no weight yet).
 __device__ __forceinline__ float weight(float x, float m) { return tc::ex2((x - (m == kNegInf ? 0.f : m)) * kLog2e); }
 

@@ -16,7 +16,11 @@
 //   warps 2..5  one row per thread: its queries to shared memory, then per block the
 //               scores out of TMEM, the running maximum (moved only when a score
 //               passes it by 2^8), P = exp(s - m) as bf16 into TMEM (half a step of
-//               2^-8 off, as in the layer's forward), the sum in fp32
+//               2^-8 off), the sum of what is rounded there in fp32
+// O is divided as in the layer's forward: a replaced row's by the sum of the rounded weights (an MMA against a tile of
+// ones, into columns that hold S where there are keys: eight MMAs of N = 16 a block, no time that shows), so that a dominant key's V is
+// not scaled by its weight's rounding; an ordinary row's by the sum of the weights before that (256 columns a CTA leave
+// no room beside S, and summing the rounded ones in the row warps took the chunks below from 91 to 99 us).
 // S_{j+1} is issued as soon as the rows have copied S_j to registers, before P V_j.
 //   ordinary row   s = q . k / 8
 //   replaced row   s = a[j] + r[i - j], 32 keys at a time, from shared memory: one stretch
@@ -48,9 +52,10 @@ constexpr int NTHREADS = 192;
 constexpr uint32_t TILE_BYTES = 128 * 64 * 2;
 constexpr uint32_t TMEM_COLS = 256;
 constexpr uint32_t TO_COL = 128, TP_COL = 192;  // S in 0..127, O, P
+constexpr uint32_t TSUM_COL = 0;                // the rows' sums of rounded weights, of items without keys (and without S)
 
 // shared memory map (offsets from a 1024-aligned base)
-constexpr uint32_t SM_Q = 0;
+constexpr uint32_t SM_Q = 0;                           // of an item without keys: 16 rows x 128 bytes of ones
 constexpr uint32_t SM_K = SM_Q + TILE_BYTES;
 constexpr uint32_t SM_V = SM_K + NST * TILE_BYTES;
 constexpr int PAT_PITCH = 33;                          // floats: a warp's reads of its 32 rows hit distinct banks
@@ -155,8 +160,14 @@ __device__ __forceinline__ void exp_quarter(const uint32_t (&v)[32], uint64_t un
     tmem_st16(tP + 16 * Q, pw);
 }
 
-// This warp's 32 O rows times f.
-__device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
+// This warp's 32 O rows times f, with `sums` the sums of their rounded weights too.
+__device__ __forceinline__ void rescale_o(uint32_t tmem, float f, bool sums) {
+    const uint32_t tO = tmem + TO_COL;
+    if (sums) {
+        const float x = __uint_as_float(tmem_ld1(tmem + TSUM_COL));
+        tmem_wait_ld();
+        tmem_st1(tmem + TSUM_COL, __float_as_uint(x * f));
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint32_t ov[32];
@@ -174,7 +185,8 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
 // on weights that are at most as large as the new maximum's), P goes to TMEM and
 // its sum to l.  first: O holds nothing yet.
 __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool first, float unit, float& m, float& l,
-                                          uint32_t tO, uint32_t tP) {
+                                          uint32_t tmem, bool sums) {
+    const uint32_t tP = tmem + TP_COL;
     float mx2[2] = {kNegInf, kNegInf};
 #pragma unroll
     for (int e = 0; e < 32; e += 2) mx2[(e >> 1) & 1] = max3(mx2[(e >> 1) & 1], v[e], v[e + 1]);
@@ -185,7 +197,7 @@ __device__ __forceinline__ void chunk_out(const float (&v)[32], int c, bool firs
         if (grow) m = mx;
         l *= f;
         tmem_wait_st();
-        if (!first) rescale_o(tO, f);
+        if (!first) rescale_o(tmem, f, sums);
 #pragma unroll 1
         for (int d = c + 1; d < 4; ++d) {
             uint32_t pw[16];
@@ -276,7 +288,7 @@ __device__ __noinline__ float2 near_block(float m, float l, bool primed, bool ne
             for (int e = 0; e < 32; ++e)
                 if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = kNegInf;
         }
-        chunk_out(v, c, first, kLog2e, m, l, tmem + TO_COL, tmem + TP_COL);
+        chunk_out(v, c, first, kLog2e, m, l, tmem, true);
     }
     __syncwarp();  // the buffer has been read
     return make_float2(m, l);
@@ -325,7 +337,7 @@ __device__ __noinline__ float2 far_block(float m, float l, bool primed, bool nex
             if (n >= FAR_BUFS || next) far_copy(edge, key - 16 * FAR_BUFS);
             else copies_commit();
         }
-        chunk_out(v, c, first, kLog2e, m, l, tmem + TO_COL, tmem + TP_COL);
+        chunk_out(v, c, first, kLog2e, m, l, tmem, true);
     }
     return make_float2(m, l);
 }
@@ -382,7 +394,7 @@ __device__ __noinline__ float2 mixed_block(float m, float l, float unit, int vis
 #pragma unroll
         for (int e = 0; e < 32; ++e)
             if (e >= left || ((bad >> ((32 * c + e) >> lb)) & 1u)) v[e] = kNegInf;
-        chunk_out(v, c, first, unit, m, l, tmem + TO_COL, tmem + TP_COL);
+        chunk_out(v, c, first, unit, m, l, tmem, !keyed);
     }
     return make_float2(m, l);
 }
@@ -506,7 +518,7 @@ __device__ __noinline__ RowResult plain_rows(float unit, int vis, uint32_t tmem,
             exp_quarter<1>(w[1], unit2, nm2, l2, tmem + TP_COL);
             const float2 s2 = split_f32x2(add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3])));
             l += s2.x + s2.y;
-            if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tmem + TO_COL, f);
+            if (i > 0 && __any_sync(~0u, f != 1.f)) rescale_o(tmem, f, false);
         }
         hand_over();
     }
@@ -704,6 +716,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         // ------------------------------------------------ MMA issuer (one elected lane, as in the layer's kernels)
         const uint32_t idS = idesc_bf16(128, 128, 0, 0);  // Q (K-major) x K (K-major)
         const uint32_t idO = idesc_bf16(128, 64, 0, 1);   // P (TMEM) x V (MN-major)
+        const uint32_t idSum = idesc_bf16(128, 16, 0, 0); // P (TMEM) x ones (K-major)
         constexpr uint64_t kStage = TILE_BYTES >> 4;
         const uint64_t dQ = sw128_desc(sbase + SM_Q), dK0 = sw128_desc(sbase + SM_K), dV0 = sw128_desc(sbase + SM_V);
         int nk = 0, nv = 0, nq = 0;  // S and P V products issued, items with queries
@@ -748,6 +761,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         mma_ts(tmem + TO_COL, tmem + TP_COL + 8 * k, dV0 + s * kStage + 128 * k, idO, (i > 0 || k > 0) ? 1u : 0u);
+                    if (!keyed) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tmem + TSUM_COL, tmem + TP_COL + 8 * k, dQ + 2 * (k & 3), idSum, (i > 0 || k > 0) ? 1u : 0u);
+                    }
                     mma_commit(bar_o);
                     mma_commit(bar_ve + 8 * s);
                 }
@@ -784,6 +802,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     st_shared_v4(sbase + SM_Q + row * 128 + ((c ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
                 fence_proxy_async_smem();
                 mbar_arrive_warp(bar_q);
+            } else if (x.nt > 0) {  // ones, which the first P V waits for along with P
+                const uint32_t one2 = 0x3f803f80u;
+                st_shared_v4(sbase + SM_Q + row * 16, one2, one2, one2, one2);
+                fence_proxy_async_smem();
             }
             const bool rep = info.out >= 0 && info.replaced;
             const uint32_t reps = __ballot_sync(~0u, rep && info.vis > 0);
@@ -838,6 +860,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 waited = true;
             }
             // ---- the rows out, or a piece of them
+            // A replaced row is divided by the sum of its rounded weights (see the kernel for few rows), an ordinary one, as in
+            // the layer's forward, by that of the weights: a column of sums has no room beside S.
+            float f = 1.f;
+            if (!keyed && x.nt > 0) {
+                f = __uint_as_float(tmem_ld1(tmem_rows + TSUM_COL));
+                tmem_wait_ld();
+                f = by_rounded(l, f);
+            }
             constexpr int SLOT = BM * (kHeadDim + 2);
             float* slot = p.slots + ((size_t)blockIdx.x * 2 + (x.t0 == 0)) * SLOT;
 #pragma unroll
@@ -852,8 +882,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    const float4 o = make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                                                 __uint_as_float(ov[e + 3]));
+                    const float4 o = make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f,
+                                                 __uint_as_float(ov[e + 2]) * f, __uint_as_float(ov[e + 3]) * f);
                     if (x.pieces > 1) __stcg(reinterpret_cast<float4*>(slot + row * kHeadDim + 32 * c + e), o);
                     else finish_row<PREFIX>(p, info, 32 * c + e, o, m, l);
                 }
