@@ -366,6 +366,11 @@ SAF_API saf_status saf_kv_append(const saf_paged_kv *kv,
  *            (every call leaves its counters zero again; after a call that
  *            saf_device_status reports as failed, zero it once more), not shared
  *            with the layer's entry points, and not used by two calls at once.
+ * The layout of the work follows from T_q: with more than 24 rows (T_q * H / H_kv)
+ * to a K/V head, a sequence with fewer new tokens still fills blocks of 128 rows per
+ * query head, and its keys are read once for each.  A batch of long chunks and
+ * single tokens is better given as two calls.
+ * Weights are rounded to bf16 for their product with V; scores and sums are fp32.
  * Limits: B * H * T_q and max_len (with a prefix prefix_len + max_len) are at
  * most 2^31 - 4097, else SAF_ERR_INVALID_ARG (saf_paged_workspace_size:
  * (size_t)-1).  The work of the longest lengths allowed, whatever the lengths

@@ -7,9 +7,10 @@
 // pairs (2i, 2i+1) lie inside a chunk.  Rows q, k, v of a token form one axis of
 // H + 2 H_kv rows.
 //
-// HBM bounds long appends: 8 x 4096 tokens of 12 heads (3 replaced), with the rotated
-// keys beside the cache, 290 MB in 60 us, 4.9 TB/s (44 us at a plain copy's rate).  A
-// step's few rows take 2 to 5 us, a launch's latency.
+// Long appends: 8 x 4096 tokens of 12 heads (3 replaced), with the rotated keys beside
+// the cache, 290 MB in 59 us, 4.9 TB/s (44 us at a plain copy's rate): HBM half busy by
+// its counters, issue slots two thirds, 26 warps an SM that each wait for four rows
+// of 128 bytes and end.  A step's few rows take 2 to 5 us, a launch's latency.
 #include <algorithm>
 
 #include "saf_paged.cuh"

@@ -32,10 +32,10 @@
 // One new token makes this a stream of K and V at a few flops per byte: HBM
 // bounds it, so the warp-level MMAs are enough, and the kernel is built for bytes
 // in flight and short chains.  64 sequences of 16384 keys, 12 heads (3 replaced, no K):
-// 2.82 GB in 420 us, 6.7 TB/s (a plain copy's rate).  Short work shows the
-// latencies instead: 8 sequences of up to 4096 keys 24 us (10 at that rate), 512 keys
-// of one sequence 8.5 us; five drafted tokens of 32 sequences (four heads to a K/V
-// head: 20 rows, four warps for want of registers) 98 us against 52.
+// 2.82 GB in 416 to 425 us, 6.6 to 6.8 TB/s (a plain copy's rate).  Short work shows the
+// latencies instead: 8 sequences of up to 4096 keys 22 us (10 at that rate), 512 keys
+// of one sequence 8.7 us; five drafted tokens of 32 sequences (four heads to a K/V
+// head: 20 rows, four warps for want of registers) 95 us against 52.
 // Rows on the M side, sixteen at least, would leave most of an MMA to padding: with the
 // keys there instead, 96 registers hold a warp's rows and eight warps fit (the first
 // of these shapes 515 -> 418 us).

@@ -38,7 +38,7 @@
 // memory allow no more) the latencies of their own chain of load, maximum, exponential
 // and store show.
 // 4 sequences of up to 8192 keys, chunks of 500, 12 heads (3 replaced): 92 us, of which
-// 75 this kernel; prefix of 16384 under 256 sequences, 32 heads (8 replaced) on 8: 84 us.
+// about 80 this kernel; prefix of 16384 under 256 sequences, 32 heads (8 replaced) on 8: 86 us.
 #include "saf_paged.cuh"
 
 namespace saf {
@@ -87,9 +87,11 @@ struct TcPiece {
 static_assert(sizeof(TcPiece) <= 48, "item slot");
 // What the rows of a warp have in common.  It and the item stay in shared memory
 // and are read where they are wanted: the row loops below are functions of their
-// own, with a handful of scalar arguments, so that nothing crowds the 128 scores of
+// own, with a handful of scalar arguments, so that little crowds the 128 scores of
 // a row out of the registers or goes through the stack (with two CTAs' shared
-// memory taken, L1 is too small to hold one: spilled, the loops took twice as long).
+// memory taken, L1 is too small to hold one: spilled, the loops took twice as long;
+// what is left is about 50 to 70 bytes a call of a loop, and 160 in the kernel
+// around them).
 struct WarpRows {
     const float *a, *r;    // of the head of the first row that looks scores up, at local key 0 (r: at its own position, r[-j])
     const float *a0, *r0;  // the arrays, a0 at local key 0 of head 0

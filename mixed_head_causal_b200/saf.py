@@ -564,7 +564,8 @@ def paged_attn(q, kv: PagedKV, page_table, seq_lens, alpha=None, rho=None, mask=
     seq_lens [B], page_table [B, max_pages] int32 and q_lens (None, or [B] int32)
     are device tensors, read by the kernels; max_len bounds the lengths.  mask,
     alpha, rho: the replaced heads and their pattern ([H, pattern_len], at least
-    max_len long).  Callers that run many steps pass out, lse and a workspace
+    max_len long).  A batch that mixes long chunks and single tokens is better
+    given as two calls (see include/saf.h).  Callers that run many steps pass out, lse and a workspace
     (new_paged_workspace).  No gradient is kept: a cache is not trained through
     (the layer's own backward is mixed_attn_bwd)."""
     return _paged(kv, stream, q, None, 0, page_table, seq_lens, alpha, rho, mask, q_lens, max_len, out, lse, workspace)
