@@ -527,6 +527,20 @@ __device__ __noinline__ RowResult plain_rows(float unit, int vis, uint32_t tmem,
     return {m, l, 1};
 }
 
+// The blocks of a warp without a row that has a token, in an item without keys: there is no S to read, and no one reads
+// what its rows come to.
+__device__ __noinline__ RowResult idle_rows(int ni, int nk, int nv) {
+    const int nt = item_of(ni).nt;
+    int k0 = (item_of(ni).t0 + nt) * BN;
+    for (int i = 0; i < nt; ++i, ++nv) {
+        k0 -= BN;
+        uint32_t bad;
+        if (!block_arrived(false, nk, nv, bad) || !p_free(i == 0, nv) || !clear_dead(ni, nv, k0, bad)) return {kNegInf, 0.f, 0};
+        hand_over();
+    }
+    return {kNegInf, 0.f, 1};
+}
+
 // The blocks of a warp with replaced rows (off, edge: see near_block and far_block).
 __device__ __noinline__ RowResult pattern_rows(float unit, int vis, uint32_t tmem, int ni, int nk, int nv, int off, int edge) {
     float m = kNegInf, l = 0.f;
@@ -844,7 +858,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             __syncwarp();
             RowResult res;  // running maximum (in the row's units), sum
-            if (!reps) {
+            if (!reps && !x.keyed && vmin >= x.len) {
+                res = idle_rows(ni, nk, nv);
+            } else if (!reps) {
                 res = plain_rows(unit, info.vis, tmem_rows, ni, nk, nv);
             } else {
                 const int edge = (int)(((r_first + off - 15) & ~3ll) - r_first);
