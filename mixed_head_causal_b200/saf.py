@@ -394,7 +394,7 @@ class _Guards:
 
     def __init__(self, device, stream):
         if stream is not None and stream.device != device:     # (its kernels would run on the other device's memory)
-            raise ValueError(f"stream: a stream of {stream.device}, the cache or table is on {device}")
+            raise ValueError(f"stream: a stream of {stream.device}, the tensors are on {device}")
         self._guards = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
@@ -588,9 +588,11 @@ def paged_attn_prefix(q, kv: PagedKV, prefix_table, prefix_len: int, page_table,
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:
-    """Reads and clears the device error word of `workspace` (synchronous)."""
-    return int(load().saf_device_status(_ptr(workspace), workspace.numel() * workspace.element_size(),
-                                        _stream_ptr(stream)))
+    """Reads and clears the device error word of `workspace` (synchronous: waits
+    for `stream`, by default the current stream of the workspace's device)."""
+    with _Guards(workspace.device, stream):
+        return int(load().saf_device_status(_ptr(workspace), workspace.numel() * workspace.element_size(),
+                                            _current_stream(workspace.device)))
 
 
 def selftest_wait_timeout(workspace: torch.Tensor, limit_cycles: int = 1 << 20, stream=None) -> None:

@@ -165,3 +165,32 @@ def test_row_limit(lib):
     assert lib.saf_paged_workspace_size(128, 4, 2, 1 << 22, 0) == none
     assert lib.saf_paged_workspace_size(1, 256, 1, (1 << 25) - 1, 0) == none     # (256 times that is a multiple of 2^32, less 256)
     assert lib.saf_paged_workspace_size(1, 256, 1, 1 << 24, 40) == none
+
+
+def test_device_status_waits_on_the_workspaces_device(monkeypatch):
+    """Whatever device is current, as the serving calls run on their cache's."""
+    entered, calls = [], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *exc):
+            entered.append(None)
+
+    def status(ptr, nbytes, stream):
+        calls.append((ptr, nbytes, stream, list(entered)))
+        return saf.SAF_OK
+
+    device = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(saf, "_current_stream", lambda d: {device: 77}[d])
+    monkeypatch.setattr(saf, "load", lambda: SimpleNamespace(saf_device_status=status))
+    ws = SimpleNamespace(device=device, data_ptr=lambda: FAKE, numel=lambda: 512, element_size=lambda: 1)
+    assert saf.device_status(ws) == saf.SAF_OK
+    assert calls == [(FAKE, 512, 77, [device])] and entered == [device, None]
+    with pytest.raises(ValueError, match="stream"):
+        saf.device_status(ws, stream=SimpleNamespace(device=torch.device("cuda", 0)))
